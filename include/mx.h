@@ -289,6 +289,134 @@ mx_status mx_a4w4_gemm_grouped_act_quant_plan(int64_t E, int64_t R_max, int64_t 
 mx_status mx_a4w4_gemm_grouped_mx_plan(int64_t N, int64_t K, int64_t rows_hint, char* buf,
                                        size_t buf_len);
 
+/* ------------------------------------------------------------------------------------------
+ * A key/value cache in MXFP4, in pages, and the attention that reads it: what a decoder
+ * layer runs between the GEMM that makes its queries, keys and values and the one that takes
+ * the attention's output. Keys and values are quantized row by row with the rule at the top
+ * of this file (blocks of 32 along the head), so a cached head costs D * 17/32 bytes per key
+ * and per value instead of 2 D.
+ *
+ * Cache layout. A cache is num_pages pages of page_size tokens (a power of two, 16 .. 1024)
+ * for `heads` key/value heads of D elements (64, 128 or 256): [page][head] blocks of
+ * page_size * D * 17 / 16 bytes. One block holds, with n = page_size / 16 tiles of 16 tokens
+ * and m = D / 32 scale blocks per token,
+ *   K codes   [n][m][16 tokens][16 bytes]    one 32-block each, canonical order
+ *   V codes   [n][4][16 bytes][m][4 tokens]  byte b of block j of token 4g + i at [g][b][j][i]
+ *   K scales  [n][m][16 tokens]              E8M0
+ *   V scales  [n][16 tokens][m]              E8M0
+ * (every region is an MFMA operand in lane order). Slot s is token s % page_size of page
+ * s / page_size. A cache needs no clearing: bytes of tokens that were never written do not
+ * reach any result. The rows given to mx_kv_write must be finite.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Size in bytes of a cache. 0 when num_pages is not in [1, 2^31), heads not in [1, 1024], or
+ * page_size or D is not one of those above. */
+size_t mx_kv_cache_bytes(int64_t num_pages, int64_t page_size, int64_t heads, int64_t D);
+
+/*
+ * Block tables and slot maps from the requests' lengths, on the device (no host round trip,
+ * fit for stream capture). Request b holds old_lens[b] tokens and shall hold new_lens[b]: it
+ * takes ceil(new / page_size) - ceil(old / page_size) pages from the stack of free pages, or
+ * gives its last pages back when that is negative (an ended request: new_lens[b] = 0; drafts
+ * taken back: fewer than old).
+ *  old_lens, new_lens: [B] int32. block_table: [B, max_blocks] int32, updated in place: entry
+ *    [b][i] is the page of tokens i * page_size ..; only the entries of new pages are written.
+ *  free_pages: [capacity] int32, the stack, updated in place; free_count: [1] int32, its
+ *    height; free_count_out: [1] int32, the height afterwards (may be free_count itself).
+ *    Pages given back are pushed first, in the requests' order and each request's in order of
+ *    its tokens; then pages are popped in the requests' order.
+ *  cu_q: [B+1] int32, where each request's new rows start: the sums of max(new - old, 0).
+ *  slots: [T_max] int64 and positions: [T_max] int32, the slot and the position of every new
+ *    row; both are -1 from row cu_q[B] on (so a padded batch writes nothing).
+ *  status: [1] int32: 0; or the number of pages the stack lacks; or -1 when a length is
+ *    negative or past max_blocks * page_size, the new rows exceed T_max, free_count is not in
+ *    [0, capacity], or the pages given back do not fit the stack. Unless it is 0, nothing
+ *    moves: the table and the stack keep their contents, free_count_out is free_count, cu_q
+ *    is all 0 and every slot is -1.
+ * Because the lengths and the height are read from one place and written to another, calling
+ * it twice with the same arguments gives the same result. A page must stand on the stack or
+ * in the table's held entries once. workspace: mx_kv_tables_workspace_bytes(B, T_max) bytes
+ * (0 for small batches: NULL), 16-byte aligned. Requires 0 <= B <= 2^20, 1 <= max_blocks,
+ * 0 <= T_max <= 2^30, 0 <= capacity < 2^31 and page_size as above. Errors: MX_ERR_NULL,
+ * MX_ERR_SHAPE, MX_ERR_ALIGN (4 bytes; slots 8; workspace 16), MX_ERR_WORKSPACE,
+ * MX_ERR_DEVICE, MX_ERR_HIP.
+ */
+mx_status mx_kv_tables(const int32_t* old_lens, const int32_t* new_lens, int64_t B, int64_t page_size,
+                       int32_t* block_table, int64_t max_blocks, int32_t* free_pages, int64_t capacity,
+                       const int32_t* free_count, int32_t* free_count_out, int64_t T_max, int32_t* cu_q,
+                       int64_t* slots, int32_t* positions, int32_t* status, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace mx_kv_tables needs. 0 for sizes it refuses. */
+size_t mx_kv_tables_workspace_bytes(int64_t B, int64_t T_max);
+
+/*
+ * Quantizes T rows of keys and of values into the cache: row t's head h goes to slot
+ * slots[t]. k_bf16, v_bf16: row t's heads are heads * D consecutive bf16 values at element
+ * t * k_stride (t * v_stride), so columns of a fused projection's output can be given as they
+ * are; strides are multiples of 8. slots: [T] int64; a slot outside [0, num_pages *
+ * page_size) writes nothing. A slot named twice ends up with bytes of either row: give each
+ * once. T == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (k, v, cache: 16
+ * bytes; slots: 8), MX_ERR_DEVICE, MX_ERR_HIP.
+ */
+mx_status mx_kv_write(const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride,
+                      const int64_t* slots, int64_t T, void* cache, int64_t num_pages, int64_t page_size,
+                      int64_t heads, int64_t D, hipStream_t stream);
+
+/*
+ * The inverse: the values that the cache holds at `slots`, in bf16 (exact; a value below
+ * bf16's least subnormal becomes 0 or that): k_bf16, v_bf16 [T, heads, D] dense. Rows whose
+ * slot is outside the cache are left as they were. Same requirements and errors.
+ */
+mx_status mx_kv_read(const void* cache, int64_t num_pages, int64_t page_size, int64_t heads, int64_t D,
+                     const int64_t* slots, int64_t T, void* k_bf16, void* v_bf16, hipStream_t stream);
+
+/*
+ * Attention of bf16 queries over the cache. Request b's rows are cu_q[b] .. cu_q[b+1] - 1 of
+ * q; with n of them and L = kv_lens[b] cached tokens, row i stands at position L - n + i (its
+ * own key is already in the cache) and
+ *   out[i][h] = sum_j p_j V[j][h / (heads_q / heads)],  p = softmax_j(scale * q[i][h] . K[j])
+ * over the tokens j < L that it sees: with causal != 0 those at j <= its position, and with
+ * window > 0 (causal only) those at j > its position - window. A row that sees nothing is 0.
+ *  q_bf16: row t's heads_q * D values at element t * q_stride; out_bf16 likewise with
+ *    out_stride >= heads_q * D (strides are multiples of 8). heads_q is a multiple of heads.
+ *    Rows from cu_q[B] on are neither read nor written.
+ *  block_table: [B, max_blocks] int32; entries of tokens that no row sees are not read. An
+ *    entry outside [0, num_pages) makes its tokens unseen.
+ *  cu_q: [B+1] int32, non-decreasing from 0 (clamped to [0, T]); kv_lens: [B] int32 (clamped
+ *    to [0, max_blocks * page_size]).
+ *  max_q, max_kv: the most rows and the longest kv_len of any request: they size the launch
+ *    and nothing else (any value >= 1 is correct).
+ *  workspace: partial results where the tokens of a request are split over the chip, of
+ *    mx_kv_attention_workspace_bytes(...) bytes; always optional: with a NULL or smaller one
+ *    the tokens are split less or not at all.
+ * Queries are used exactly (not quantized); scores and the softmax's maximum and sum are
+ * FP32; the weights are rounded to bf16 for the product with V, whose sum is FP32; the result
+ * is rounded once. Output is bitwise reproducible for the same arguments. Requires 0 <= T <=
+ * 2^30, 0 <= B <= 2^20, 1 <= max_blocks, scale finite and > 0, |scale * q . K| below 1e38 and
+ * the cache's sizes as above. T == 0 or B == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE,
+ * MX_ERR_ALIGN (q, out, cache, workspace: 16 bytes; tables: 4), MX_ERR_DEVICE, MX_ERR_HIP.
+ */
+mx_status mx_kv_attention(const void* q_bf16, int64_t q_stride, const void* cache, int64_t num_pages,
+                          int64_t page_size, const int32_t* block_table, int64_t max_blocks,
+                          const int32_t* cu_q, const int32_t* kv_lens, int64_t B, int64_t T, int64_t heads_q,
+                          int64_t heads, int64_t D, int64_t max_q, int64_t max_kv, int32_t causal,
+                          int64_t window, float scale, void* out_bf16, int64_t out_stride, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace mx_kv_attention can use for these sizes. 0 where it needs none or refuses them. */
+size_t mx_kv_attention_workspace_bytes(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t D,
+                                       int64_t max_q, int64_t max_kv, int64_t window);
+
+/*
+ * Introspection (host only, no GPU needed): the kernels mx_kv_attention would launch for these
+ * sizes with workspace_bytes of workspace, as the other *_plan calls. Errors: MX_ERR_SHAPE,
+ * MX_ERR_NULL (buf NULL or buf_len 0).
+ */
+mx_status mx_kv_attention_plan(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t D, int64_t max_q,
+                               int64_t max_kv, int64_t window, size_t workspace_bytes, char* buf,
+                               size_t buf_len);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,17 @@ SIGNATURES = {
     "mx_a16w4_gemm": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp]),
     "mx_a4w4_gemm_noalloc": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp]),
     "mx_noalloc_scratch_bytes": (_c_sz, []),
+    "mx_kv_cache_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "mx_kv_tables": (_c_int, [_vp, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _vp, _c_i64, _vp, _vp, _vp, _vp,
+                              _vp, _c_sz, _vp]),
+    "mx_kv_tables_workspace_bytes": (_c_sz, [_c_i64, _c_i64]),
+    "mx_kv_write": (_c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _vp]),
+    "mx_kv_read": (_c_int, [_vp, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _vp]),
+    "mx_kv_attention": (_c_int, [_vp, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64,
+                                 _c_i64, _c_i64, _c_i64, ctypes.c_int32, _c_i64, ctypes.c_float, _vp, _c_i64, _vp, _c_sz,
+                                 _vp]),
+    "mx_kv_attention_workspace_bytes": (_c_sz, [_c_i64] * 8),
+    "mx_kv_attention_plan": (_c_int, [_c_i64] * 8 + [_c_sz, ctypes.c_char_p, _c_sz]),
     "mx_calib_read": (_c_int, [_vp, _c_sz, _c_i64, _vp, _vp]),
     "mx_calib_mfma": (_c_int, [_c_i64, _c_i64, _vp, _vp]),
     "mx_calib_mfma_flops": (ctypes.c_double, [_c_i64, _c_i64]),
@@ -415,6 +426,204 @@ def mx_a4w4_gemm_grouped_plan(E: int, R_max: int, T: int, N: int, K: int, rows_h
     return buf.value.decode()
 
 
+# ----------------------------------------------------------------------------- the MXFP4 key/value cache
+
+def mx_kv_cache_bytes(num_pages: int, page_size: int, heads: int, D: int) -> int:
+    """Bytes of a paged MXFP4 key/value cache (0 for sizes the library refuses)."""
+    return int(lib().mx_kv_cache_bytes(int(num_pages), int(page_size), int(heads), int(D)))
+
+
+def _kv_pages(cache, page_size, heads, D):
+    """Pages that fit the uint8 buffer `cache`."""
+    torch = _torch()
+    _need(cache, "cache", torch.uint8)
+    per = mx_kv_cache_bytes(1, page_size, heads, D)
+    if per == 0:
+        raise MxError(MX_ERR_SHAPE, f"kv cache with page_size={page_size}, heads={heads}, D={D}")
+    pages = cache.numel() // per
+    if pages < 1:
+        raise ValueError(f"cache holds {cache.numel()} bytes, one page needs {per}")
+    return pages
+
+
+def _new(shape, dtype, device, stream):
+    """A new tensor of the stream that the call runs on, so that torch neither hands out memory
+    the current stream still uses nor reuses it under a kernel of `stream`."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows3(t, name):
+    """(rows, heads, D, row stride) of a bf16 [rows, heads, D] tensor whose rows are dense (a
+    slice of columns of a wider row-major tensor is)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D, got shape {tuple(t.shape)}")
+    T, H, D = (int(d) for d in t.shape)
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must have dense rows, got strides {t.stride()}")
+    return T, H, D, int(t.stride(0)) if T > 1 else H * D
+
+
+def _here(t, name):
+    """Device pointer of a tensor checked by _rows3."""
+    torch = _torch()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device.index is not None and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def mx_kv_tables_workspace_bytes(B: int, max_rows: int) -> int:
+    return int(lib().mx_kv_tables_workspace_bytes(int(B), int(max_rows)))
+
+
+def mx_kv_tables(old_lens, new_lens, block_table, free_pages, free_count, page_size: int, max_rows: int, cu_q=None,
+                 slots=None, positions=None, free_count_out=None, status=None, workspace=None, stream=None):
+    """Block tables and slots from the requests' lengths (int32 [B], before and after the step):
+    block_table [B, max_blocks] and the stack free_pages [capacity] (both int32) are updated in
+    place. Returns (cu_q int32 [B+1], slots int64 [max_rows], positions int32 [max_rows],
+    free_count_out int32 [1], status int32 [1]); status 0 means done (see mx.h for the rest)."""
+    torch = _torch()
+    i32 = torch.int32
+    _need(block_table, "block_table", i32)
+    B, max_blocks = _dims2(block_table, "block_table")
+    _need(old_lens, "old_lens", i32, shape=(B,))
+    _need(new_lens, "new_lens", i32, shape=(B,))
+    _need(free_pages, "free_pages", i32)
+    _need(free_count, "free_count", i32, min_numel=1)
+    dev = block_table.device
+    max_rows = int(max_rows)
+    cu_q = cu_q if cu_q is not None else _new((B + 1,), i32, dev, stream)
+    slots = slots if slots is not None else _new((max(max_rows, 0),), torch.int64, dev, stream)
+    positions = positions if positions is not None else _new((max(max_rows, 0),), i32, dev, stream)
+    free_count_out = free_count_out if free_count_out is not None else _new((1,), i32, dev, stream)
+    status = status if status is not None else _new((1,), i32, dev, stream)
+    _need(cu_q, "cu_q", i32, min_numel=B + 1)
+    _need(slots, "slots", torch.int64, min_numel=max_rows)
+    _need(positions, "positions", i32, min_numel=max_rows)
+    _need(free_count_out, "free_count_out", i32, min_numel=1)
+    _need(status, "status", i32, min_numel=1)
+    nbytes = mx_kv_tables_workspace_bytes(B, max_rows)
+    if nbytes and workspace is None:
+        workspace = _new((nbytes,), torch.uint8, dev, stream)
+    ws_ptr, ws_bytes = (None, 0)
+    if nbytes:
+        ws_ptr, ws_bytes = _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size()
+    _check(lib().mx_kv_tables(
+        _dev(old_lens, i32, "old_lens"), _dev(new_lens, i32, "new_lens"), B, int(page_size),
+        _dev(block_table, i32, "block_table"), max_blocks, _dev(free_pages, i32, "free_pages"), free_pages.numel(),
+        _dev(free_count, i32, "free_count"), _dev(free_count_out, i32, "free_count_out"), max_rows,
+        _dev(cu_q, i32, "cu_q"), _dev(slots, torch.int64, "slots"), _dev(positions, i32, "positions"),
+        _dev(status, i32, "status"), ws_ptr, ws_bytes, _stream_ptr(stream)), "mx_kv_tables")
+    return cu_q, slots, positions, free_count_out, status
+
+
+def mx_kv_write(k_bf16, v_bf16, slots, cache, page_size: int, stream=None) -> None:
+    """Quantize keys and values [T, heads, D] bf16 (rows dense, any row stride) to MXFP4 into the
+    cache's slots (int64 [T]; a slot outside the cache writes nothing)."""
+    torch = _torch()
+    T, heads, D, k_stride = _rows3(k_bf16, "k_bf16")
+    if tuple(v_bf16.shape) != tuple(k_bf16.shape):
+        raise ValueError(f"v_bf16 must have shape {tuple(k_bf16.shape)}, got {tuple(v_bf16.shape)}")
+    v_stride = _rows3(v_bf16, "v_bf16")[3]
+    _need(slots, "slots", torch.int64, min_numel=T)
+    pages = _kv_pages(cache, page_size, heads, D)
+    if T == 0:
+        return
+    _check(lib().mx_kv_write(_here(k_bf16, "k_bf16"), k_stride, _here(v_bf16, "v_bf16"), v_stride,
+                             _dev(slots, torch.int64, "slots"), T, _dev(cache, torch.uint8, "cache"), pages,
+                             int(page_size), heads, D, _stream_ptr(stream)), "mx_kv_write")
+
+
+def mx_kv_read(cache, slots, heads: int, D: int, page_size: int, k_out=None, v_out=None, stream=None):
+    """(k, v) bf16 [T, heads, D]: the values the cache holds at `slots` (int64 [T]); rows whose
+    slot is outside the cache are left as they were."""
+    torch = _torch()
+    _need(slots, "slots", torch.int64)
+    T = slots.numel()
+    pages = _kv_pages(cache, page_size, heads, D)
+    k = k_out if k_out is not None else _new((T, heads, D), torch.bfloat16, cache.device, stream)
+    v = v_out if v_out is not None else _new((T, heads, D), torch.bfloat16, cache.device, stream)
+    _need(k, "k_out", torch.bfloat16, shape=(T, heads, D))
+    _need(v, "v_out", torch.bfloat16, shape=(T, heads, D))
+    if T == 0:
+        return k, v
+    _check(lib().mx_kv_read(_dev(cache, torch.uint8, "cache"), pages, int(page_size), int(heads), int(D),
+                            _dev(slots, torch.int64, "slots"), T, _dev(k, torch.bfloat16, "k_out"),
+                            _dev(v, torch.bfloat16, "v_out"), _stream_ptr(stream)), "mx_kv_read")
+    return k, v
+
+
+def mx_kv_attention_workspace_bytes(B: int, T: int, heads_q: int, heads: int, D: int, max_q: int, max_kv: int,
+                                    window: int = 0) -> int:
+    return int(lib().mx_kv_attention_workspace_bytes(int(B), int(T), int(heads_q), int(heads), int(D), int(max_q),
+                                                     int(max_kv), int(window)))
+
+
+def mx_kv_attention(q_bf16, cache, block_table, cu_q, kv_lens, heads: int, page_size: int, causal: bool = True,
+                    window: int = 0, scale=None, max_q=None, max_kv=None, out=None, workspace=None, stream=None):
+    """Attention of q [T, heads_q, D] bf16 (rows dense, any row stride) over the paged cache:
+    request b's rows are cu_q[b] .. cu_q[b+1] - 1 (int32 [B+1]) over kv_lens[b] cached tokens
+    (int32 [B]) in the pages block_table[b] (int32 [B, max_blocks]), its last row at the last
+    token. Returns out [T, heads_q, D] bf16.
+
+    scale defaults to D ** -0.5. max_q and max_kv (the most rows and the longest length of any
+    request; hints only) default to T and to the table's width. workspace: a device tensor for
+    partial results, None to allocate mx_kv_attention_workspace_bytes(...) bytes through torch,
+    or False to pass none.
+    """
+    torch = _torch()
+    i32 = torch.int32
+    T, heads_q, D, q_stride = _rows3(q_bf16, "q_bf16")
+    _need(block_table, "block_table", i32)
+    B, max_blocks = _dims2(block_table, "block_table")
+    _need(cu_q, "cu_q", i32, min_numel=B + 1)
+    _need(kv_lens, "kv_lens", i32, min_numel=B)
+    pages = _kv_pages(cache, page_size, heads, D)
+    o = out if out is not None else _new((T, heads_q, D), torch.bfloat16, q_bf16.device, stream)
+    if tuple(o.shape) != (T, heads_q, D):
+        raise ValueError(f"out must have shape {(T, heads_q, D)}, got {tuple(o.shape)}")
+    out_stride = _rows3(o, "out")[3]
+    if T == 0 or B == 0:
+        return o
+    max_q = int(max_q) if max_q is not None else T
+    max_kv = int(max_kv) if max_kv is not None else max_blocks * int(page_size)
+    scale = float(scale) if scale is not None else D ** -0.5
+    if workspace is None:
+        nbytes = mx_kv_attention_workspace_bytes(B, T, heads_q, heads, D, max_q, max_kv, window)
+        workspace = _new((nbytes,), torch.uint8, q_bf16.device, stream) if nbytes else False
+    ws_ptr, ws_bytes = (None, 0)
+    if workspace is not False:
+        ws_ptr, ws_bytes = _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size()
+    _check(lib().mx_kv_attention(
+        _here(q_bf16, "q_bf16"), q_stride, _dev(cache, torch.uint8, "cache"), pages, int(page_size),
+        _dev(block_table, i32, "block_table"), max_blocks, _dev(cu_q, i32, "cu_q"), _dev(kv_lens, i32, "kv_lens"), B, T,
+        heads_q, int(heads), D, max_q, max_kv, int(bool(causal)), int(window), scale, _here(o, "out"), out_stride,
+        ws_ptr, ws_bytes, _stream_ptr(stream)), "mx_kv_attention")
+    return o
+
+
+def mx_kv_attention_plan(B: int, T: int, heads_q: int, heads: int, D: int, max_q: int, max_kv: int, window: int = 0,
+                         workspace_bytes=None) -> str:
+    """Kernels mx_kv_attention launches for these sizes; workspace_bytes defaults to what it
+    allocates when given no workspace."""
+    if workspace_bytes is None:
+        workspace_bytes = mx_kv_attention_workspace_bytes(B, T, heads_q, heads, D, max_q, max_kv, window)
+    buf = ctypes.create_string_buffer(256)
+    _check(lib().mx_kv_attention_plan(int(B), int(T), int(heads_q), int(heads), int(D), int(max_q), int(max_kv),
+                                      int(window), int(workspace_bytes), buf, len(buf)), "mx_kv_attention_plan")
+    return buf.value.decode()
+
+
 def mx_calib_read(buf, ctas: int, sink, stream=None) -> None:
     """One streaming-read launch over the whole of `buf` (a contiguous device tensor whose
     byte size is a multiple of 16); `sink` is a device tensor of at least 4 bytes."""
@@ -475,7 +684,8 @@ __all__ = [
     "mx_prepare_weight_packed", "mx_unprepare_weight", "mx_quant_act", "mx_a4w4_gemm", "mx_a4w4_gemm_grouped",
     "mx_a4w4_gemm_plan", "mx_a16w4_gemm_plan", "mx_a4w4_gemm_grouped_plan", "mx_a4w4_gemm_grouped_act_quant",
     "mx_a4w4_gemm_grouped_act_quant_plan", "mx_a4w4_gemm_grouped_mx", "mx_a4w4_gemm_grouped_mx_plan",
-    "mx_moe_combine", "mx_a16w4_gemm", "MX_ACT_SILU", "MX_ACT_SWIGLU", "mx_calib_read", "mx_calib_mfma",
+    "mx_moe_combine", "mx_a16w4_gemm", "mx_kv_cache_bytes", "mx_kv_tables", "mx_kv_tables_workspace_bytes",
+    "mx_kv_write", "mx_kv_read", "mx_kv_attention", "mx_kv_attention_workspace_bytes", "mx_kv_attention_plan", "MX_ACT_SILU", "MX_ACT_SWIGLU", "mx_calib_read", "mx_calib_mfma",
     "mx_calib_mfma_flops", "mx_calib_mfma_operands", "mx_calib_mfma_operands_flops",
     "mx_calib_mfma_operands_clock",
 ]

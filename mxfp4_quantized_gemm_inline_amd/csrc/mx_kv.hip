@@ -1,0 +1,288 @@
+// mx_kv.hip - the paged MXFP4 key/value cache: block tables and slots from the requests'
+// lengths, the write (quantizing) and the read back.
+#include "mx_kv.h"
+
+#include "mx_device.h"
+
+namespace mx {
+namespace {
+
+// ------------------------------------------------------------------------------- tables
+//
+// Three running sums over the requests decide everything: new rows, pages taken, pages given
+// back. With cnt pages on the stack, `back` given back and `take` taken, the stack after the
+// pushes is virtual[i] = free_pages[i] (i < cnt) or the (i - cnt)-th page given back, and the
+// k-th page taken is virtual[cnt + back - 1 - k]. No step needs another's writes: entries
+// below cnt are only read, those from cnt on only written, rows of the table either give
+// (read) or take (written), so every row and page is worked out on its own from the sums.
+// Bound: launch latency at decoding sizes; one dependent chain of searches per row beyond.
+
+constexpr int kScanThreads = 1024;
+constexpr int kOneGroupRequests = 1024;  // whose sums fit 12 KB of LDS
+// Rows that one workgroup fills by itself; past them the sums go through the workspace to a
+// second launch over the whole chip.
+constexpr int kOneGroupRows = 4096;
+constexpr uint32_t kCap = (1u << 31) - 1;  // sums saturate here: larger than any valid one
+
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kCap); }  // a, b <= kCap
+
+struct KvSums {
+  int ok, cnt, back, take, rows;
+};
+
+__device__ __forceinline__ int pages_of(int len, int lg) { return (int)(((int64_t)len + (1 << lg) - 1) >> lg); }
+
+// The largest b < n with sums[b] <= x, sums non-decreasing with sums[0] = 0 and x >= 0.
+__device__ __forceinline__ int find(const int32_t* sums, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Inclusive scan over the workgroup of three saturating sums.
+__device__ __forceinline__ void scan3(uint32_t (&x)[3], uint32_t (*wave)[3]) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+      const uint32_t y = __shfl_up(x[c], d);
+      if (lane >= d) x[c] = sat_add(x[c], y);
+    }
+  __syncthreads();  // the previous round's reads of wave[] are over
+  if (lane == 63)
+#pragma unroll
+    for (int c = 0; c < 3; ++c) wave[w][c] = x[c];
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < 3; ++c) {
+    uint32_t base = 0;
+    for (int i = 0; i < w; ++i) base = sat_add(base, wave[i][c]);
+    x[c] = sat_add(x[c], base);
+  }
+}
+
+// The sums by one workgroup, to rows/take/back[0 .. B] (LDS or workspace; entry 0 is 0), and
+// what they come to.
+__device__ KvSums tables_scan(const KvTablesArgs& a, int32_t* rows, int32_t* take, int32_t* back) {
+  __shared__ uint32_t wave[kScanThreads / 64][3];
+  __shared__ uint32_t total[3];
+  __shared__ int bad;
+  if (threadIdx.x == 0) {
+    rows[0] = take[0] = back[0] = 0;
+    bad = 0;
+    total[0] = total[1] = total[2] = 0;
+  }
+  __syncthreads();
+  for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
+    const int b = b0 + (int)threadIdx.x;
+    uint32_t x[3] = {0, 0, 0};
+    if (b < a.B) {
+      const int o = a.old_lens[b], n = a.new_lens[b];
+      if (o < 0 || n < 0 || pages_of(max(o, n), a.log2_page) > a.max_blocks) {
+        bad = 1;
+      } else {
+        const int held = pages_of(o, a.log2_page), want = pages_of(n, a.log2_page);
+        x[0] = (uint32_t)max(n - o, 0);
+        x[1] = (uint32_t)max(want - held, 0);
+        x[2] = (uint32_t)max(held - want, 0);
+      }
+    }
+    scan3(x, wave);
+#pragma unroll
+    for (int c = 0; c < 3; ++c) x[c] = sat_add(x[c], total[c]);
+    if (b < a.B) {
+      rows[b + 1] = (int32_t)x[0];
+      take[b + 1] = (int32_t)x[1];
+      back[b + 1] = (int32_t)x[2];
+    }
+    __syncthreads();
+    if (threadIdx.x == kScanThreads - 1)
+#pragma unroll
+      for (int c = 0; c < 3; ++c) total[c] = x[c];
+    __syncthreads();
+  }
+  KvSums s;
+  s.cnt = *a.free_count;
+  s.rows = (int)total[0];
+  s.take = (int)total[1];
+  s.back = (int)total[2];
+  const bool valid = !bad && s.cnt >= 0 && s.cnt <= a.capacity && s.rows <= a.T_max &&
+                     (int64_t)s.cnt + s.back - s.take <= a.capacity;
+  const int64_t lacks = (int64_t)s.take - s.back - s.cnt;
+  s.ok = valid && lacks <= 0;
+  __syncthreads();  // everybody has read free_count, which may be free_count_out
+  if (threadIdx.x == 0) {
+    *a.status = !valid ? -1 : lacks > 0 ? (int)lacks : 0;
+    *a.free_count_out = s.ok ? s.cnt + s.back - s.take : s.cnt;
+  }
+  for (int b = (int)threadIdx.x; b <= a.B; b += kScanThreads) a.cu_q[b] = s.ok ? rows[b] : 0;
+  return s;
+}
+
+// The i-th page given back.
+__device__ __forceinline__ int given_back(const KvTablesArgs& a, const int32_t* back, int i) {
+  const int b = find(back, a.B, i);
+  return a.block_table[(int64_t)b * a.max_blocks + pages_of(a.new_lens[b], a.log2_page) + i - back[b]];
+}
+
+__device__ __forceinline__ void tables_fill(const KvTablesArgs& a, const KvSums& s, const int32_t* rows,
+                                            const int32_t* take, const int32_t* back, int first, int step) {
+  const int P = 1 << a.log2_page;
+  for (int t = first; t < a.T_max; t += step) {
+    int64_t slot = -1;
+    int pos = -1;
+    if (s.ok && t < s.rows) {
+      const int b = find(rows, a.B, t);
+      pos = a.old_lens[b] + t - rows[b];
+      const int blk = pos >> a.log2_page, held = pages_of(a.old_lens[b], a.log2_page);
+      int32_t* entry = a.block_table + (int64_t)b * a.max_blocks + blk;
+      int page;
+      if (blk < held) {
+        page = *entry;
+      } else {
+        const int v = s.cnt + s.back - 1 - (take[b] + blk - held);
+        page = v < s.cnt ? a.free_pages[v] : given_back(a, back, v - s.cnt);
+        if ((pos & (P - 1)) == 0) *entry = page;  // a new page's first token is always a new row
+      }
+      slot = ((int64_t)page << a.log2_page) + (pos & (P - 1));
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+  }
+  if (s.ok)
+    for (int i = first; i < s.back - s.take; i += step) a.free_pages[s.cnt + i] = given_back(a, back, i);
+}
+
+__global__ __launch_bounds__(kScanThreads) void k_kv_tables(KvTablesArgs a) {
+  __shared__ int32_t rows[kOneGroupRequests + 1], take[kOneGroupRequests + 1], back[kOneGroupRequests + 1];
+  const KvSums s = tables_scan(a, rows, take, back);
+  tables_fill(a, s, rows, take, back, (int)threadIdx.x, kScanThreads);
+}
+
+// workspace: KvSums, padded to 32 bytes, then rows, take and back of B + 1 entries each
+__global__ __launch_bounds__(kScanThreads) void k_kv_tables_scan(KvTablesArgs a, int32_t* ws) {
+  int32_t* sums = ws + 8;
+  const KvSums s = tables_scan(a, sums, sums + a.B + 1, sums + 2 * (a.B + 1));
+  if (threadIdx.x == 0) *reinterpret_cast<KvSums*>(ws) = s;
+}
+
+__global__ __launch_bounds__(256) void k_kv_tables_fill(KvTablesArgs a, const int32_t* ws) {
+  const KvSums s = *reinterpret_cast<const KvSums*>(ws);
+  const int32_t* sums = ws + 8;
+  tables_fill(a, s, sums, sums + a.B + 1, sums + 2 * (a.B + 1), (int)(blockIdx.x * 256 + threadIdx.x),
+              (int)(gridDim.x * 256));
+}
+
+bool one_group(int64_t B, int64_t T_max) { return B <= kOneGroupRequests && T_max <= kOneGroupRows; }
+
+// ------------------------------------------------------------------------------- write, read
+
+// One thread per 32-block of one head of one row: the library's block quantizer, its 16 code
+// bytes and its scale byte, for the key and for the value.
+__global__ __launch_bounds__(256) void k_kv_write(const uint16_t* __restrict__ k, int64_t k_stride,
+                                                  const uint16_t* __restrict__ v, int64_t v_stride,
+                                                  const int64_t* __restrict__ slots, int64_t units,
+                                                  uint8_t* __restrict__ cache, int64_t num_slots, int lg, int heads,
+                                                  int D) {
+  const int m = D / 32, per = heads * m;
+  const KvLayout L = {1 << lg, D};
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+    const int64_t t = u / per;
+    const int h = (int)(u % per) / m, d = (int)(u % m) * 32;
+    const int64_t slot = slots[t];
+    if (slot < 0 || slot >= num_slots) continue;
+    const int tok = (int)(slot & (L.P - 1));
+    uint8_t* blk = cache + ((slot >> lg) * heads + h) * L.block_bytes();
+    uint32_t x[16], q[4];
+    load_block(k + t * k_stride + h * D + d, x);
+    blk[L.k_scale(tok, d)] = (uint8_t)quant_block(x, q);
+    *reinterpret_cast<uint4*>(blk + L.k_code(tok, d)) = make_uint4(q[0], q[1], q[2], q[3]);
+    load_block(v + t * v_stride + h * D + d, x);
+    blk[L.v_scale(tok, d)] = (uint8_t)quant_block(x, q);
+#pragma unroll
+    for (int b = 0; b < 16; ++b) blk[L.v_code(tok, d + 2 * b)] = (uint8_t)(q[b / 4] >> (8 * (b % 4)));
+  }
+}
+
+// 8 codes of one scale, as bf16 (an E2M1 value times a power of two is exact in bf16).
+__device__ __forceinline__ uint4 decode8(uint32_t codes, uint32_t scale) {
+  const float sc = __builtin_bit_cast(float, scale << 23);  // 0 acts as 2^-127
+  return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, sc, 0)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, sc, 1)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, sc, 2)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, sc, 3)));
+}
+
+// One thread per 8 elements of one head of one row.
+__global__ __launch_bounds__(256) void k_kv_read(const uint8_t* __restrict__ cache, int64_t num_slots, int lg,
+                                                 int heads, int D, const int64_t* __restrict__ slots, int64_t units,
+                                                 uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
+  const int m = D / 8, per = heads * m;
+  const KvLayout L = {1 << lg, D};
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+    const int64_t t = u / per;
+    const int h = (int)(u % per) / m, d = (int)(u % m) * 8;
+    const int64_t slot = slots[t];
+    if (slot < 0 || slot >= num_slots) continue;
+    const int tok = (int)(slot & (L.P - 1));
+    const uint8_t* blk = cache + ((slot >> lg) * heads + h) * L.block_bytes();
+    *reinterpret_cast<uint4*>(k + u * 8) =
+        decode8(*reinterpret_cast<const uint32_t*>(blk + L.k_code(tok, d)), blk[L.k_scale(tok, d)]);
+    uint32_t c = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) c |= (uint32_t)blk[L.v_code(tok, d + 2 * b)] << (8 * b);
+    *reinterpret_cast<uint4*>(v + u * 8) = decode8(c, blk[L.v_scale(tok, d)]);
+  }
+}
+
+}  // namespace
+
+// Workgroups of 256 threads for `units` threads' worth of work; past 2^20 they loop (a launch
+// holds fewer than 2^32 threads).
+static unsigned groups_of(int64_t units) { return (unsigned)min((units + 255) / 256, (int64_t)1 << 20); }
+
+size_t kv_tables_workspace_bytes(int64_t B, int64_t T_max) {
+  return one_group(B, T_max) ? 0 : (size_t)(32 + 12 * (B + 1));
+}
+
+hipError_t launch_kv_tables(const KvTablesArgs& a, void* workspace, hipStream_t st) {
+  if (one_group(a.B, a.T_max)) {
+    hipLaunchKernelGGL(k_kv_tables, dim3(1), dim3(kScanThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  hipLaunchKernelGGL(k_kv_tables_scan, dim3(1), dim3(kScanThreads), 0, st, a, ws);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  // one row per thread up to a few rounds of the chip; pages given back beyond that loop
+  const int groups = min(max((a.T_max + 255) / 256, 64), 4096);
+  hipLaunchKernelGGL(k_kv_tables_fill, dim3((unsigned)groups), dim3(256), 0, st, a, (const int32_t*)ws);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slots,
+                           int64_t T, void* cache, int64_t num_pages, int64_t P, int64_t heads, int64_t D,
+                           hipStream_t st) {
+  const int64_t units = T * heads * (D / 32);
+  const int lg = __builtin_ctzll((unsigned long long)P);
+  hipLaunchKernelGGL(k_kv_write, dim3(groups_of(units)), dim3(256), 0, st,
+                     static_cast<const uint16_t*>(k), k_stride, static_cast<const uint16_t*>(v), v_stride, slots, units,
+                     static_cast<uint8_t*>(cache), num_pages * P, lg, (int)heads, (int)D);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const void* cache, int64_t num_pages, int64_t P, int64_t heads, int64_t D,
+                          const int64_t* slots, int64_t T, void* k, void* v, hipStream_t st) {
+  const int64_t units = T * heads * (D / 8);
+  const int lg = __builtin_ctzll((unsigned long long)P);
+  hipLaunchKernelGGL(k_kv_read, dim3(groups_of(units)), dim3(256), 0, st,
+                     static_cast<const uint8_t*>(cache), num_pages * P, lg, (int)heads, (int)D, slots, units,
+                     static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
+  return hipGetLastError();
+}
+
+}  // namespace mx

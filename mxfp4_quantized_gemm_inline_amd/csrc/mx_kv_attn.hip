@@ -4,6 +4,7 @@
 //   s_j = scale q . K[j],  out = sum_j exp(s_j - m) V[j] / sum_j exp(s_j - m),  m = max_j s_j,
 // in one pass over the tokens: with the running maximum m, sum l and unscaled output o, a
 // block of tokens with maximum m' multiplies l and o by exp(m - max(m, m')) and adds its own.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -14,111 +15,587 @@ namespace mx {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLag = 8.f;
 constexpr float kLowest = -3.0e38f;  // the running maximum before any token: below every score
 
-// Value of one E2M1 code: sign, two exponent bits, one mantissa bit; subnormal 0.5.
-__device__ __forceinline__ float e2m1(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float v = e ? (float)((2u + m) << (e - 1)) * 0.5f : 0.5f * (float)m;
-  return (c & 8u) ? -v : v;
+// ------------------------------------------------------------------------------- row tiles
+//
+// The rows of one request and one key/value head: query row i and head g of the group are row
+// r = i G + g of n G rows that read the same keys and values. A row tile is R of them.
+
+struct RowTile {
+  int b, q0, n, rb, rows;  // request, its first query row and count, first row of the tile, rows in it
+  int len;                 // cached tokens
+  int lo, hi;              // tokens that some row of the tile sees (lo a multiple of 16; hi <= lo: none)
+  __device__ int pos(int r, int G) const { return len - n + r / G; }
+};
+
+__device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+// The tokens that a row at `pos` sees.
+__device__ __forceinline__ int row_end(const KvAttnArgs& a, int len, int pos) {
+  return a.causal ? clamp_int(pos + 1, 0, len) : len;
 }
-__device__ __forceinline__ float e8m0(uint32_t s) {
-  return __builtin_bit_cast(float, s ? s << 23 : 0x00400000u);
+__device__ __forceinline__ int row_begin(const KvAttnArgs& a, int pos) {
+  return a.window ? max(max(pos, 0) - a.window + 1, 0) : 0;
 }
 
-// One wave per (row, query head); lane = token in blocks of 64 for the scores, lane = elements
-// lane, lane + 64, .. for the output.
-__global__ __launch_bounds__(64) void k_kv_attn_row(KvAttnArgs a) {
-  __shared__ float q[256], p[64];
-  __shared__ int page[64];
-  const int lane = threadIdx.x, t = (int)(blockIdx.x / a.Hq), hq = (int)(blockIdx.x % a.Hq), h = hq / a.G;
+// Row tile `rb` rows into request b; false where the request has no such rows.
+__device__ __forceinline__ bool row_tile_of(const KvAttnArgs& a, int R, int b, int rb, RowTile& w) {
+  w.b = b;
+  w.q0 = clamp_int(a.cu_q[b], 0, a.T);
+  w.n = clamp_int(a.cu_q[b + 1], w.q0, a.T) - w.q0;
+  w.rb = rb;
+  w.rows = min(R, w.n * a.G - rb);
+  if (w.rows <= 0) return false;
+  w.len = (int)min((int64_t)max(a.kv_lens[b], 0), (int64_t)a.max_blocks << a.log2_page);
+  w.lo = row_begin(a, w.pos(rb, a.G)) & ~15;
+  w.hi = row_end(a, w.len, w.pos(rb + w.rows - 1, a.G));
+  return true;
+}
+
+// Numbering row tiles without a sum over the requests: request b's tiles are
+// floor(cu_q[b] G / R) + b on, which leaves room for its ceil(n G / R) and never decreases. The
+// wave searches 64 requests at a time for the last one that starts at or before `tile`.
+__device__ __forceinline__ int first_tile(const KvAttnArgs& a, int R, int b) {
+  return (int)((int64_t)clamp_int(a.cu_q[b], 0, a.T) * a.G / R) + b;
+}
+__device__ __forceinline__ bool find_row_tile(const KvAttnArgs& a, int R, int tile, RowTile& w) {
+  const int lane = threadIdx.x & 63;
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
+    const int step = (hi - lo + 63) / 64, b = lo + lane * step;
+    const bool at = b < hi && first_tile(a, R, b) <= tile;
+    lo += (max((int)__popcll(__ballot(at)), 1) - 1) * step;
+    hi = min(hi, lo + step);
   }
-  const int b = lo;
-  const int r0 = min(max(a.cu_q[b], 0), a.T), r1 = min(max(a.cu_q[b + 1], r0), a.T);
-  if (t < r0 || t >= r1) return;
-  const int64_t most = (int64_t)a.max_blocks << a.log2_page;
-  const int len = (int)min((int64_t)max(a.kv_lens[b], 0), most);
-  const int pos = len - (r1 - r0) + (t - r0);
-  const int end = a.causal ? min(len, pos + 1) : len;
-  const int begin = a.window ? max(pos - a.window + 1, 0) : 0;
-  for (int d = lane; d < a.D; d += 64) {
-    const uint32_t x = a.q[(int64_t)t * a.q_stride + hq * a.D + d];
-    q[d] = __builtin_bit_cast(float, x << 16);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  const int rb = tile - first_tile(a, R, lo);
+  return rb >= 0 && rb < (1 << 30) / R && row_tile_of(a, R, lo, rb * R, w);
+}
+int row_tiles(const KvAttnSizes& z, int R) { return (int)(z.T * (z.Hq / z.H) / R + z.B); }
+
+// The tokens [lo, hi) of a row tile in splits of C; the last of at most S takes what is left.
+__device__ __forceinline__ int splits_of(const RowTile& w, int C, int S) {
+  return clamp_int((w.hi - w.lo + C - 1) / C, 1, S);
+}
+
+// ------------------------------------------------------------------------------- operands
+
+// A query row in two 8-bit floats. With 2^e the power that brings the row's largest element
+// into [128, 256), hi = e4m3(q 2^-e) keeps four of bf16's eight significant bits and
+// lo = e4m3((q 2^-e - hi) 2^5) the other four: together exact for elements down to 2^-13 of the
+// largest and to 2^-21 of it below. So the keys enter the scaled MFMA as they lie in the cache,
+// 4-bit with their scale bytes, and none is ever converted; one product more pays for that with
+// the same matrix time as bf16 and no vector time.
+__device__ __forceinline__ void split_fp8(const uint32_t (&x)[8], float down, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float f[4], r[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = __builtin_bit_cast(float, x[2 * j + i] << 16) * down;
+      f[2 * i + 1] = __builtin_bit_cast(float, x[2 * j + i] & 0xFFFF0000u) * down;
+    }
+    uint32_t h = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+    h = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], h, true);
+    r[0] = (f[0] - __builtin_amdgcn_cvt_f32_fp8(h, 0)) * 32.f;
+    r[1] = (f[1] - __builtin_amdgcn_cvt_f32_fp8(h, 1)) * 32.f;
+    r[2] = (f[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 32.f;
+    r[3] = (f[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 32.f;
+    uint32_t l = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
+    l = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], l, true);
+    hi[j] = h;
+    lo[j] = l;
+  }
+}
+// Scale byte of hi for a row whose largest exponent field is E (lo's is 5 less); the row is
+// multiplied by 2^(127 - byte) before it is split.
+__device__ __forceinline__ uint32_t query_scale(uint32_t E) { return E > 12u ? E - 7u : 5u; }
+
+// Largest exponent field of bf16 pairs.
+__device__ __forceinline__ uint32_t top_exponent(const uint4& u, uint32_t E) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+    E = max(E, max((w >> 7) & 0xFFu, (w >> 23) & 0xFFu));
+  }
+  return E;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){x, y}, bf16x2));
+}
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(bf16x8, (u32x4){a, b, c, d});
+}
+
+// Byte I of a word (a pair of codes) times its scale, the scale byte J of another word.
+template <int I>
+__device__ __forceinline__ uint32_t decode2(uint32_t codes, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, I));
+}
+template <int J>
+__device__ __forceinline__ float scale_at(uint32_t w) {
+  if constexpr (J == 3) return __builtin_bit_cast(float, (w >> 1) & 0x7F800000u);
+  return __builtin_bit_cast(float, ((w >> (8 * J)) & 0xFFu) << 23);
+}
+
+// ------------------------------------------------------------------------------- few rows
+//
+// Decoding and drafts: one workgroup of four waves takes a tile of 16 NT rows and C tokens of one
+// head, each wave a quarter of them on its own, 32 tokens a step, the next step's operands in
+// flight. The transposed products put a query row in each of the 16 columns:
+//   S^T (16 tokens x 16 rows) = K Q^T    scaled 16x16x128 MFMA, A = K codes from the cache,
+//   O^T (D x 16 rows)        += V^T P^T  bf16 16x16x32 MFMA, A = V decoded in registers.
+// A lane's four scores of each of two token tiles (tokens 4g..4g+3) are, rounded to bf16, its
+// eight elements of P^T: no exchange between lanes. V's codes lie in the cache so that one word
+// holds four tokens of an element pair; two conversions and two byte permutations make the
+// operands of the pair's two rows of V^T.
+// Bound: HBM, the tokens' 17/16 D bytes; the conversions take about half of the vector issue.
+
+template <int D>
+struct TokenTile {  // one lane's share of 16 tokens
+  static constexpr int M = D / 32;
+  u32x4 k[(D + 127) / 128];
+  uint32_t ks[(D + 127) / 128];
+  uint32_t v[M];   // word j: the lane's element pair of scale block j, four tokens
+  uint32_t vs[M];  // the 4 M scale bytes of its four tokens
+
+  __device__ __forceinline__ void load(const uint8_t* blk, int P, int in_page, int lane) {
+    const int g = lane >> 4;
+    const uint8_t* kc = blk + in_page * (8 * D);
+    const uint8_t* kb = blk + P * D + in_page * (D / 2);
+    if constexpr (D == 64) {
+      k[0] = *reinterpret_cast<const u32x4*>(kc + (lane & 31) * 16);
+      ks[0] = kb[lane & 31];
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 128; ++c) {
+        k[c] = *reinterpret_cast<const u32x4*>(kc + c * 1024 + lane * 16);
+        ks[c] = kb[c * 64 + lane];
+      }
+    }
+    const uint8_t* vc = blk + P * (D / 2) + in_page * (8 * D) + lane * (4 * M);
+    const uint8_t* vb = blk + P * D + P * M + in_page * (16 * M) + g * (4 * M);
+    typedef uint32_t words __attribute__((ext_vector_type(M)));
+    const words a = *reinterpret_cast<const words*>(vc), b = *reinterpret_cast<const words*>(vb);
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      v[j] = a[j];
+      vs[j] = b[j];
+    }
+  }
+  // Scale of block j of the lane's token i: byte (i M + j) of vs.
+  template <int I, int J>
+  __device__ __forceinline__ float scale() const {
+    return scale_at<(I * M + J) % 4>(vs[(I * M + J) / 4]);
+  }
+  // Scales of the tokens outside [lo, hi) become 0 (2^-127): their codes, never written or
+  // written by another request, cannot be infinite then. t: the lane's first token.
+  __device__ __forceinline__ void mask(int t, int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t + i < lo || t + i >= hi) {
+        if constexpr (M == 2) vs[i / 2] &= i % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+        else
+#pragma unroll
+          for (int j = 0; j < M / 4; ++j) vs[i * (M / 4) + j] = 0;
+      }
+  }
+};
+
+constexpr int kFewWaves = 4;
+
+template <int D, int NT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_kv_attn_few(KvAttnArgs a, int rows_most, int C, int S,
+                                                                float* __restrict__ part, float2* __restrict__ part_ml) {
+  constexpr int R = 16 * NT, M = D / 32, KC = (D + 127) / 128, LD = D + 4;
+  __shared__ float o_all[kFewWaves][16][LD];
+  __shared__ float2 ml_all[kFewWaves][R];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
+  const int split = (int)(blockIdx.x % S), h = (int)(blockIdx.x / S % a.H);
+  RowTile w;
+  if (!find_row_tile(a, R, (int)(blockIdx.x / S / a.H), w)) return;
+  if (w.n * a.G > rows_most) return;  // the other kernel's
+  const int splits = splits_of(w, C, S);
+  if (split >= splits) return;
+
+  // the queries, split in two
+  v8i q_hi[NT][KC], q_lo[NT][KC];
+  uint32_t q_sc[NT];
+  int row_lo[NT], row_hi[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = w.rb + min(16 * nt + col, w.rows - 1);  // columns past the last row repeat it
+    const uint16_t* src = a.q + (int64_t)(w.q0 + r / a.G) * a.q_stride + (h * a.G + r % a.G) * D;
+    uint4 x[2 * KC];
+    uint32_t E = 0;
+    if constexpr (D == 64) {  // each lane group 16 elements
+      x[0] = reinterpret_cast<const uint4*>(src)[2 * g];
+      x[1] = reinterpret_cast<const uint4*>(src)[2 * g + 1];
+      E = top_exponent(x[1], top_exponent(x[0], 0));
+      E = max(E, (uint32_t)__shfl_xor((int)E, 16));
+      E = max(E, (uint32_t)__shfl_xor((int)E, 32));
+    } else {
+      uint4 y[4 * KC];
+#pragma unroll
+      for (int c = 0; c < KC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // bytes 0..15: elements 16 g, bytes 16..31: 64 + 16 g
+          y[4 * c + i] = reinterpret_cast<const uint4*>(src + 128 * c + 64 * (i / 2) + 16 * g)[i % 2];
+#pragma unroll
+      for (int i = 0; i < 4 * KC; ++i) E = top_exponent(y[i], E);
+      E = max(E, (uint32_t)__shfl_xor((int)E, 16));
+      E = max(E, (uint32_t)__shfl_xor((int)E, 32));
+      const float down = __builtin_bit_cast(float, (254u - query_scale(E)) << 23);
+#pragma unroll
+      for (int c = 0; c < KC; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 u = y[4 * c + 2 * i], v = y[4 * c + 2 * i + 1];
+          const uint32_t e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+          uint32_t hi[4], lo[4];
+          split_fp8(e, down, hi, lo);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            q_hi[nt][c][4 * i + j] = (int)hi[j];
+            q_lo[nt][c][4 * i + j] = (int)lo[j];
+          }
+        }
+    }
+    const uint32_t sc = query_scale(E);
+    if constexpr (D == 64) {
+      // one 16x16x128 product takes both parts: k < 64 is hi (bytes 0..15), k >= 64 lo, over the
+      // same keys given twice (lane groups 2 and 3 load what 0 and 1 do)
+      const float down = __builtin_bit_cast(float, (254u - sc) << 23);
+      const uint32_t e[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+      uint32_t hi[4], lo[4];
+      split_fp8(e, down, hi, lo);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        q_hi[nt][0][j] = (int)hi[j];
+        q_hi[nt][0][4 + j] = (int)lo[j];
+      }
+      q_sc[nt] = g < 2 ? sc : sc - 5u;
+    } else {
+      q_sc[nt] = sc;
+    }
+    const int pos = w.pos(r, a.G);
+    row_lo[nt] = row_begin(a, pos);
+    row_hi[nt] = row_end(a, w.len, pos);
+  }
+
+  // this wave's tokens
+  const int t0 = w.lo + split * C;
+  const int t1 = split == S - 1 ? w.hi : min(w.hi, t0 + C);
+  const int share = ((t1 - t0 + 32 * kFewWaves - 1) / (32 * kFewWaves)) * 32;
+  const int w0 = t0 + wave * share, w1 = min(t1, w0 + share);
+  // a step inside [all_lo, all_hi) needs no mask
+  const int all_lo = row_begin(a, w.pos(w.rb + w.rows - 1, a.G)), all_hi = min(w1, row_end(a, w.len, w.pos(w.rb, a.G)));
+  const float c2 = a.scale * kLog2e;
+  const int P = 1 << a.log2_page;
+  const int32_t* table = a.block_table + (int64_t)w.b * a.max_blocks;
+
+  float m[NT], l[NT];
+  v4f o[NT][2 * M];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = kLowest;
+    l[nt] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2 * M; ++j) o[nt][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+  }
+
+  for (int base = w0; base < w1; base += 64 * 16) {  // 64 token tiles whose pages one load fetches
+    const int tiles = min(64, (w1 - base + 15) >> 4);
+    int page = 0;
+    bool bad = false;
+    if (lane < tiles) {
+      page = table[(base + 16 * lane) >> a.log2_page];
+      bad = page < 0 || page >= a.num_pages;
+      if (bad) page = 0;
+    }
+    const uint64_t bad_tiles = __ballot(bad);
+    auto load = [&](TokenTile<D>(&x)[2], int step) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tile = min(2 * step + i, tiles - 1);
+        const int id = __builtin_amdgcn_readlane(page, tile);
+        const uint8_t* blk = a.cache + ((int64_t)id * a.H + h) * a.block_bytes;
+        x[i].load(blk, P, ((base + 16 * tile) & (P - 1)) >> 4, lane);
+      }
+    };
+    auto compute = [&](TokenTile<D>(&x)[2], int step) {
+      const int t = base + 32 * step;
+      v4f s[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          s[nt][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            const v8i kv = {(int)x[i].k[c].x, (int)x[i].k[c].y, (int)x[i].k[c].z, (int)x[i].k[c].w, 0, 0, 0, 0};
+            s[nt][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kv, q_hi[nt][c], s[nt][i], 4, 0, 0,
+                                                                        (int)x[i].ks[c], 0, (int)q_sc[nt]);
+            if constexpr (D != 64)
+              s[nt][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kv, q_lo[nt][c], s[nt][i], 4, 0, 0,
+                                                                          (int)x[i].ks[c], 0, (int)(q_sc[nt] - 5u));
+          }
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][i][e] *= c2;
+      const uint64_t bad2 = bad_tiles >> (2 * step);
+      if (t < all_lo || t + 32 > all_hi || (bad2 & 3u)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int tt = t + 16 * i + 4 * g;
+          const bool hidden = (bad2 >> i) & 1u;
+          x[i].mask(tt, w.lo, hidden ? 0 : w1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (hidden || tt + e < row_lo[nt] || tt + e >= min(row_hi[nt], w1)) s[nt][i][e] = -INFINITY;
+        }
+      }
+      uint32_t p[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float top = fmaxf(fmaxf(fmaxf(s[nt][0][0], s[nt][0][1]), fmaxf(s[nt][0][2], s[nt][0][3])),
+                          fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
+        // The maximum in use may lag behind the true one by kLag (weights up to 2^kLag, all sums
+        // in FP32); only past that are the sums rescaled.
+        if (__any(top > m[nt] + kLag)) {
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float m1 = fmaxf(m[nt], top), alpha = __builtin_amdgcn_exp2f(m[nt] - m1);
+          m[nt] = m1;
+          l[nt] *= alpha;
+#pragma unroll
+          for (int j = 0; j < 2 * M; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][j][e] *= alpha;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            p[nt][2 * i + e / 2] = pack_bf16(__builtin_amdgcn_exp2f(s[nt][i][e] - m[nt]),
+                                             __builtin_amdgcn_exp2f(s[nt][i][e + 1] - m[nt]));
+        // the sum of the weights as the product with V takes them
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          l[nt] += __builtin_bit_cast(float, p[nt][i] << 16) + __builtin_bit_cast(float, p[nt][i] & 0xFFFF0000u);
+      }
+      static_for<M>([&](auto J) {
+        constexpr int j = J;
+        uint32_t even[4], odd[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t c0 = decode2<0>(x[i].v[j], x[i].template scale<0, j>());
+          const uint32_t c1 = decode2<1>(x[i].v[j], x[i].template scale<1, j>());
+          const uint32_t c2_ = decode2<2>(x[i].v[j], x[i].template scale<2, j>());
+          const uint32_t c3 = decode2<3>(x[i].v[j], x[i].template scale<3, j>());
+          even[2 * i] = __builtin_amdgcn_perm(c1, c0, 0x05040100);
+          even[2 * i + 1] = __builtin_amdgcn_perm(c3, c2_, 0x05040100);
+          odd[2 * i] = __builtin_amdgcn_perm(c1, c0, 0x07060302);
+          odd[2 * i + 1] = __builtin_amdgcn_perm(c3, c2_, 0x07060302);
+        }
+        const bf16x8 ve = as_bf16x8(even[0], even[1], even[2], even[3]), vo = as_bf16x8(odd[0], odd[1], odd[2], odd[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const bf16x8 pt = as_bf16x8(p[nt][0], p[nt][1], p[nt][2], p[nt][3]);
+          o[nt][2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ve, pt, o[nt][2 * j], 0, 0, 0);
+          o[nt][2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vo, pt, o[nt][2 * j + 1], 0, 0, 0);
+        }
+      });
+    };
+    const int steps = (tiles + 1) >> 1;
+    TokenTile<D> x0[2], x1[2];
+    load(x0, 0);
+    for (int st = 0; st < steps; st += 2) {
+      load(x1, min(st + 1, steps - 1));
+      compute(x0, st);
+      if (st + 1 >= steps) break;
+      load(x0, min(st + 2, steps - 1));
+      compute(x1, st + 1);
+    }
+  }
+
+  // join the waves: the largest maximum, every wave's sums at it, added in the waves' order
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    l[nt] += __shfl_xor(l[nt], 16);
+    l[nt] += __shfl_xor(l[nt], 32);
+    if (g == 0) ml_all[wave][16 * nt + col] = make_float2(m[nt], l[nt]);
   }
   __syncthreads();
-  const KvLayout L = {1 << a.log2_page, a.D};
-  const float c = a.scale * kLog2e;
-  float m = kLowest, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = begin; j0 < end; j0 += 64) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    int id = -1;
-    if (j < end) {
-      id = a.block_table[(int64_t)b * a.max_blocks + (j >> a.log2_page)];
-      if (id < 0 || id >= a.num_pages) id = -1;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float top = kLowest;
+#pragma unroll
+    for (int i = 0; i < kFewWaves; ++i) top = fmaxf(top, ml_all[i][16 * nt + col].x);
+    const float f = __builtin_amdgcn_exp2f(m[nt] - top);
+    if (nt > 0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const v4f e = o[nt][2 * j], d = o[nt][2 * j + 1];
+      *reinterpret_cast<v4f*>(&o_all[wave][col][32 * j + 8 * g]) = (v4f){e[0] * f, d[0] * f, e[1] * f, d[1] * f};
+      *reinterpret_cast<v4f*>(&o_all[wave][col][32 * j + 8 * g + 4]) = (v4f){e[2] * f, d[2] * f, e[3] * f, d[3] * f};
     }
-    if (id >= 0) {
-      const uint8_t* blk = a.cache + ((int64_t)id * a.H + h) * a.block_bytes;
-      const int tok = j & (L.P - 1);
-      float dot = 0.f;
-      for (int d = 0; d < a.D; d += 32) {
-        float part = 0.f;
-        for (int i = 0; i < 32; i += 2) {
-          const uint32_t w = blk[L.k_code(tok, d + i)];
-          part += q[d + i] * e2m1(w & 15u) + q[d + i + 1] * e2m1(w >> 4);
-        }
-        dot += part * e8m0(blk[L.k_scale(tok, d)]);
-      }
-      s = dot * c;
+    __syncthreads();
+    constexpr int E = D / 16;  // elements of a thread
+    const int cr = threadIdx.x / 16, d0 = (threadIdx.x % 16) * E;
+    if (16 * nt + cr >= w.rows) continue;
+    float M1 = kLowest, L = 0.f, x[E];
+#pragma unroll
+    for (int i = 0; i < kFewWaves; ++i) M1 = fmaxf(M1, ml_all[i][16 * nt + cr].x);
+#pragma unroll
+    for (int i = 0; i < kFewWaves; ++i) L += ml_all[i][16 * nt + cr].y * __builtin_amdgcn_exp2f(ml_all[i][16 * nt + cr].x - M1);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] = o_all[0][cr][d0 + e];
+#pragma unroll
+      for (int i = 1; i < kFewWaves; ++i) x[e] += o_all[i][cr][d0 + e];
     }
-    float top = s;
+    const int r = w.rb + 16 * nt + cr, t = w.q0 + r / a.G, hq = h * a.G + r % a.G;
+    if (splits == 1) {
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      uint16_t* dst = a.out + (int64_t)t * a.out_stride + hq * D + d0;
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-    const float m1 = fmaxf(m, top), alpha = __builtin_amdgcn_exp2f(m - m1);
-    m = m1;
-    const float w = __builtin_amdgcn_exp2f(s - m);
-    l = l * alpha + w;
-    __syncthreads();
-    p[lane] = w;
-    page[lane] = id;
-    __syncthreads();
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16(x[e] * inv, x[e + 1] * inv), pack_bf16(x[e + 2] * inv, x[e + 3] * inv));
+    } else {
+      const int64_t at = ((int64_t)split * a.T + t) * a.Hq + hq;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= alpha;
-    for (int k = 0; k < min(64, end - j0); ++k) {
-      if (page[k] < 0) continue;
-      const uint8_t* blk = a.cache + ((int64_t)page[k] * a.H + h) * a.block_bytes;
-      const int tok = (j0 + k) & (L.P - 1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = lane + 64 * i;
-        if (d >= a.D) break;
-        const uint32_t w2 = blk[L.v_code(tok, d & ~1)];
-        o[i] += p[k] * (e2m1((d & 1) ? w2 >> 4 : w2 & 15u) * e8m0(blk[L.v_scale(tok, d)]));
-      }
+      for (int e = 0; e < E; e += 4) *reinterpret_cast<v4f*>(part + at * D + d0 + e) = (v4f){x[e], x[e + 1], x[e + 2], x[e + 3]};
+      if (threadIdx.x % 16 == 0) part_ml[at] = make_float2(M1, L);
     }
   }
+}
+
+// Joins the splits of the rows that were split: one wave per row and query head.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int R, int rows_least, int rows_most, int C, int S,
+                                                      const float* __restrict__ part, const float2* __restrict__ part_ml) {
+  constexpr int E = D / 64;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= (int64_t)a.T * a.Hq) return;
+  const int t = (int)(row / a.Hq), hq = (int)(row % a.Hq);
+  int lo = 0, hi = a.B;  // the request of row t
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64, b = lo + lane * step;
+    const bool at = b < hi && a.cu_q[b] <= t;
+    lo += (max((int)__popcll(__ballot(at)), 1) - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  const int q0 = clamp_int(a.cu_q[lo], 0, a.T);
+  const int r = (t - q0) * a.G + hq % a.G;
+  RowTile w;
+  if (t < q0 || !row_tile_of(a, R, lo, r / R * R, w) || r >= w.n * a.G) return;
+  if (w.n * a.G < rows_least || w.n * a.G > rows_most) return;
+  const int splits = splits_of(w, C, S);
+  if (splits == 1) return;  // written already
+  const int64_t each = (int64_t)a.T * a.Hq;
+  float m = kLowest, l = 0.f, x[E];
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
+  for (int e = 0; e < E; ++e) x[e] = 0.f;
+  for (int s = lane; s < splits; s += 64) m = fmaxf(m, part_ml[s * each + row].x);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float2 ml = part_ml[s * each + row];
+    const float f = __builtin_amdgcn_exp2f(ml.x - m);
+    l += ml.y * f;
+    const float* src = part + (s * each + row) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] += src[e] * f;
+  }
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int i = 0; lane + 64 * i < a.D; ++i)
-    a.out[(int64_t)t * a.out_stride + hq * a.D + lane + 64 * i] = (uint16_t)f32_to_bf16_rne(o[i] * inv);
+  uint16_t* dst = a.out + (int64_t)t * a.out_stride + hq * D + lane * E;
+  if constexpr (E == 1) {
+    dst[0] = (uint16_t)f32_to_bf16_rne(x[0] * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(x[e] * inv, x[e + 1] * inv);
+  }
+}
+
+// ------------------------------------------------------------------------------- the launch
+
+constexpr int kAllRows = 0x7FFFFFFF;
+
+struct KvPlan {
+  int NT, C, S;
+};
+
+int round_up(int64_t x, int64_t n) { return (int)((x + n - 1) / n * n); }
+
+size_t part_bytes(const KvAttnSizes& z, int S) { return S <= 1 ? 0 : (size_t)(S * z.T * z.Hq * (z.D + 2) * 4); }
+
+KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
+  KvPlan p;
+  const int64_t G = z.Hq / z.H, rows = std::min(z.max_q, z.T) * G;
+  p.NT = rows <= 16 ? 1 : 2;
+  int64_t span = std::min(z.max_kv, (int64_t)1 << 30);
+  if (z.window) span = std::min(span, z.window + std::min(z.max_q, z.T) + 16);
+  const int64_t R = 16 * p.NT, groups = z.H * std::max(z.B * ((rows + R - 1) / R), z.T * G / R);
+  int64_t S = std::max<int64_t>(1, 1024 / groups);
+  p.C = std::max(256, round_up((span + S - 1) / S, 128));
+  p.S = (int)((span + p.C - 1) / p.C);
+  if (part_bytes(z, p.S) > workspace_bytes) {
+    p.C = 1 << 30;
+    p.S = 1;
+  }
+  return p;
+}
+
+template <int D>
+hipError_t launch_few(const KvAttnArgs& a, const KvAttnSizes& z, const KvPlan& p, void* ws, hipStream_t st) {
+  float* part = static_cast<float*>(ws);
+  float2* ml = reinterpret_cast<float2*>(part + (size_t)p.S * a.T * a.Hq * D);
+  const unsigned grid = (unsigned)((int64_t)row_tiles(z, 16 * p.NT) * a.H * p.S);
+  if (p.NT == 1)
+    hipLaunchKernelGGL((k_kv_attn_few<D, 1>), dim3(grid), dim3(64 * kFewWaves), 0, st, a, kAllRows, p.C, p.S, part, ml);
+  else
+    hipLaunchKernelGGL((k_kv_attn_few<D, 2>), dim3(grid), dim3(64 * kFewWaves), 0, st, a, kAllRows, p.C, p.S, part, ml);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.S == 1) return e;
+  hipLaunchKernelGGL((k_kv_attn_join<D>), dim3((unsigned)(((int64_t)a.T * a.Hq + 3) / 4)), dim3(256), 0, st, a, 16 * p.NT, 0,
+                     kAllRows, p.C, p.S, (const float*)part, (const float2*)ml);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t kv_attn_workspace_bytes(const KvAttnSizes&) { return 0; }
+size_t kv_attn_workspace_bytes(const KvAttnSizes& z) { return part_bytes(z, plan_of(z, ~(size_t)0).S); }
 
-hipError_t launch_kv_attn(const KvAttnArgs& a, const KvAttnSizes&, void*, size_t, hipStream_t st) {
-  hipLaunchKernelGGL(k_kv_attn_row, dim3((unsigned)((int64_t)a.T * a.Hq)), dim3(64), 0, st, a);
-  return hipGetLastError();
+hipError_t launch_kv_attn(const KvAttnArgs& a, const KvAttnSizes& z, void* workspace, size_t workspace_bytes,
+                          hipStream_t st) {
+  const KvPlan p = plan_of(z, workspace_bytes);
+  if (a.D == 64) return launch_few<64>(a, z, p, workspace, st);
+  if (a.D == 128) return launch_few<128>(a, z, p, workspace, st);
+  return launch_few<256>(a, z, p, workspace, st);
 }
 
-void kv_attn_plan(const KvAttnSizes& z, size_t, char* buf, size_t len) {
-  std::snprintf(buf, len, z.B == 0 || z.T == 0 ? "none" : "k_kv_attn_row");
+void kv_attn_plan(const KvAttnSizes& z, size_t workspace_bytes, char* buf, size_t len) {
+  if (z.B == 0 || z.T == 0) {
+    std::snprintf(buf, len, "none");
+    return;
+  }
+  const KvPlan p = plan_of(z, workspace_bytes);
+  std::snprintf(buf, len, "k_kv_attn_few<%d, %d> C=%d S=%d%s", (int)z.D, p.NT, p.C, p.S, p.S > 1 ? " + k_kv_attn_join" : "");
 }
 
 }  // namespace mx

@@ -393,7 +393,7 @@ mx_status mx_kv_read(const void* cache, int64_t num_pages, int64_t page_size, in
  * Queries are used exactly (not quantized); scores and the softmax's maximum and sum are
  * FP32; the weights are rounded to bf16 for the product with V, whose sum is FP32; the result
  * is rounded once. Output is bitwise reproducible for the same arguments. Requires 0 <= T <=
- * 2^30, 0 <= B <= 2^20, 1 <= max_blocks, scale finite and > 0, |scale * q . K| below 1e38 and
+ * 2^30 / heads_q, 0 <= B <= 2^22 / heads (and 2^20), 1 <= max_blocks, scale finite and > 0, |scale * q . K| below 1e38 and
  * the cache's sizes as above. T == 0 or B == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE,
  * MX_ERR_ALIGN (q, out, cache, workspace: 16 bytes; tables: 4), MX_ERR_DEVICE, MX_ERR_HIP.
  */

@@ -13,6 +13,7 @@ constexpr int64_t kMaxBatch = int64_t(1) << 20;
 constexpr int64_t kMaxStride = int64_t(1) << 32;  // elements: rows times stride stay in 63 bits
 constexpr int64_t kMaxPages = int64_t(1) << 31;
 constexpr int64_t kMaxHeads = 1024;
+constexpr int64_t kMaxTiles = int64_t(1) << 22;   // requests times heads: a launch holds under 2^32 threads
 constexpr int64_t kMaxTokens = int64_t(1) << 31;  // of one request: positions are 32-bit
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -25,7 +26,8 @@ mx_status from_hip(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_HIP; 
 
 bool attn_sizes_ok(const mx::KvAttnSizes& z) {
   return z.B >= 0 && z.B <= kMaxBatch && z.T >= 0 && z.T <= kMaxRows && z.H >= 1 && z.H <= kMaxHeads && z.Hq >= 1 &&
-         z.Hq <= kMaxHeads && z.Hq % z.H == 0 && z.T <= kMaxRows / z.Hq && head_ok(z.D) && z.max_q >= 1 &&
+         z.Hq <= kMaxHeads && z.Hq % z.H == 0 && z.T <= kMaxRows / z.Hq &&
+         z.B * z.H <= kMaxTiles && head_ok(z.D) && z.max_q >= 1 &&
          z.max_kv >= 1 && z.window >= 0;
 }
 
@@ -139,7 +141,7 @@ mx_status mx_kv_attention(const void* q_bf16, int64_t q_stride, const void* cach
   a.G = (int)(heads_q / heads);
   a.D = (int)D;
   a.causal = causal;
-  a.window = (int)(window < kMaxTokens ? window : 0);  // one past every length is none
+  a.window = (int)(window < max_blocks * page_size ? window : 0);  // one past every length is none
   a.scale = scale;
   return from_hip(mx::launch_kv_attn(a, z, workspace, workspace ? workspace_bytes : 0, stream));
 }

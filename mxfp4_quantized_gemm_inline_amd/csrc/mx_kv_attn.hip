@@ -128,6 +128,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){x, y}, bf16x2));
 }
 
+// l + the two bf16 values of a word: the sum of the weights as the product with V takes them.
+__device__ __forceinline__ float add_pair(float l, uint32_t u) {
+  return l + (__builtin_bit_cast(float, u << 16) + __builtin_bit_cast(float, u & 0xFFFF0000u));
+}
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8, (u32x4){a, b, c, d});
@@ -391,10 +396,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_attn_few(KvAttnArgs a, in
           for (int e = 0; e < 4; e += 2)
             p[nt][2 * i + e / 2] = pack_bf16(__builtin_amdgcn_exp2f(s[nt][i][e] - m[nt]),
                                              __builtin_amdgcn_exp2f(s[nt][i][e + 1] - m[nt]));
-        // the sum of the weights as the product with V takes them
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          l[nt] += __builtin_bit_cast(float, p[nt][i] << 16) + __builtin_bit_cast(float, p[nt][i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) l[nt] = add_pair(l[nt], p[nt][i]);
       }
       static_for<M>([&](auto J) {
         constexpr int j = J;
@@ -483,9 +486,280 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_attn_few(KvAttnArgs a, in
   }
 }
 
+// ------------------------------------------------------------------------------- many rows
+//
+// Prompts and chunks: one workgroup of four waves takes 128 rows of one head, each wave 32 of
+// them, and walks the tokens 64 at a time with 32-wide products of the same form:
+//   S^T (32 tokens x 32 rows) = K Q^T    scaled 32x32x64 MFMA, A = K codes from the cache,
+//   O^T (32 of D x 32 rows)  += V^T P^T  bf16 32x32x16 MFMA.
+// A wave reads the keys it needs itself (4-bit, no conversion, the waves' loads meet in L1). The
+// values are decoded once for the workgroup: each wave decodes one token tile of the next 64
+// tokens into LDS in operand order while the products of this step run; two buffers, one barrier
+// a step. Bound: matrix and vector issue alike (exponentials, conversions).
+
+constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+template <int D>
+__global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_many(KvAttnArgs a, int rows_least, int C, int S,
+                                                                  float* __restrict__ part, float2* __restrict__ part_ml) {
+  constexpr int M = D / 32, KC = D / 64;
+  __shared__ uint4 v_lds[2][4][M][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, half = lane >> 5;
+  const int split = (int)(blockIdx.x % S), h = (int)(blockIdx.x / S % a.H);
+  RowTile w;
+  // last tiles first: with a causal mask they see the most tokens
+  if (!find_row_tile(a, kManyRows, (int)(gridDim.x / S / a.H - 1 - blockIdx.x / S / a.H), w)) return;
+  if (w.n * a.G < rows_least) return;  // the other kernel's
+  const int splits = splits_of(w, C, S);
+  if (split >= splits) return;
+
+  // this wave's rows, and its lane's
+  const int wave_rows = min(32, w.rows - 32 * wave);  // may be none
+  const int first = w.rb + min(32 * wave, w.rows - 1), last = w.rb + min(32 * wave + 31, w.rows - 1);
+  const int r = min(first + col, last), pos = w.pos(r, a.G);
+  const int row_lo = row_begin(a, pos), row_hi = row_end(a, w.len, pos);
+  v8i q_hi[KC], q_lo[KC];
+  uint32_t q_sc;
+  {
+    const uint16_t* src = a.q + (int64_t)(w.q0 + r / a.G) * a.q_stride + (h * a.G + r % a.G) * D;
+    uint4 y[4 * KC];
+    uint32_t E = 0;
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // bytes 0..15: elements 16 half, bytes 16..31: 32 + 16 half
+        y[4 * c + i] = reinterpret_cast<const uint4*>(src + 64 * c + 32 * (i / 2) + 16 * half)[i % 2];
+#pragma unroll
+    for (int i = 0; i < 4 * KC; ++i) E = top_exponent(y[i], E);
+    E = max(E, (uint32_t)__shfl_xor((int)E, 32));
+    q_sc = query_scale(E);
+    const float down = __builtin_bit_cast(float, (254u - q_sc) << 23);
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 u = y[4 * c + 2 * i], v = y[4 * c + 2 * i + 1];
+        const uint32_t e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        uint32_t hi[4], lo[4];
+        split_fp8(e, down, hi, lo);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          q_hi[c][4 * i + j] = (int)hi[j];
+          q_lo[c][4 * i + j] = (int)lo[j];
+        }
+      }
+  }
+
+  // tokens: the workgroup's, and those that some row of the wave sees
+  const int t0 = w.lo + split * C;
+  const int t1 = split == S - 1 ? w.hi : min(w.hi, t0 + C);
+  const int tiles = (t1 - t0 + 15) >> 4, steps = (tiles + 3) >> 2;
+  const int wave_lo = row_begin(a, w.pos(first, a.G));
+  const int wave_hi = wave_rows > 0 ? row_end(a, w.len, w.pos(last, a.G)) : 0;
+  const int all_lo = row_begin(a, w.pos(last, a.G)), all_hi = min(t1, row_end(a, w.len, w.pos(first, a.G)));
+  const float c2 = a.scale * kLog2e;
+  const int P = 1 << a.log2_page;
+  const int32_t* table = a.block_table + (int64_t)w.b * a.max_blocks;
+
+  // pages of 64 token tiles, one a lane, for the current group of 64 and the next; -1: hidden
+  auto pages_of_group = [&](int grp) {
+    const int tile = 64 * grp + lane;
+    int id = -1;
+    if (tile < tiles) {
+      id = table[(t0 + 16 * tile) >> a.log2_page];
+      if (id < 0 || id >= a.num_pages) id = -1;
+    }
+    return id;
+  };
+  int group = 0, page0 = pages_of_group(0), page1 = pages_of_group(1);
+  auto page_at = [&](int tile) {  // tile in the current group or the next
+    return __builtin_amdgcn_readlane((tile >> 6) == group ? page0 : page1, tile & 63);
+  };
+  auto block_at = [&](int tile, int& in_page) {
+    tile = min(tile, tiles - 1);
+    in_page = ((t0 + 16 * tile) & (P - 1)) >> 4;
+    return a.cache + ((int64_t)max(page_at(tile), 0) * a.H + h) * a.block_bytes;
+  };
+
+  u32x4 k[2][KC];
+  uint32_t ks[2][KC];
+  auto load_k = [&](int step) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      int in0, in1;
+      const uint8_t* b0 = block_at(4 * step + 2 * x, in0);
+      const uint8_t* b1 = block_at(4 * step + 2 * x + 1, in1);
+      const uint8_t* blk = (lane & 16) ? b1 : b0;
+      const int in_page = (lane & 16) ? in1 : in0;
+      const uint8_t* kc = blk + in_page * (8 * D) + half * 256 + (lane & 15) * 16;
+      const uint8_t* kb = blk + P * D + in_page * (D / 2) + half * 16 + (lane & 15);
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        k[x][c] = *reinterpret_cast<const u32x4*>(kc + c * 512);
+        ks[x][c] = kb[c * 32];
+      }
+    }
+  };
+  typedef uint32_t words __attribute__((ext_vector_type(M)));
+  words v, vs;  // the wave's token tile of a step: as in TokenTile
+  auto load_v = [&](int step) {
+    int in_page;
+    const uint8_t* blk = block_at(4 * step + wave, in_page);
+    v = *reinterpret_cast<const words*>(blk + P * (D / 2) + in_page * (8 * D) + lane * (4 * M));
+    vs = *reinterpret_cast<const words*>(blk + P * D + P * M + in_page * (16 * M) + (lane >> 4) * (4 * M));
+  };
+  auto decode_v = [&](int step, int buf) {
+    const int tile = 4 * step + wave, t = t0 + 16 * tile;
+    TokenTile<D> x;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      x.v[j] = v[j];
+      x.vs[j] = vs[j];
+    }
+    const bool hidden = tile >= tiles || page_at(min(tile, tiles - 1)) < 0;
+    if (t + 16 > t1 || hidden) x.mask(t + 4 * (lane >> 4), w.lo, hidden ? 0 : t1);
+    uint2* dst = reinterpret_cast<uint2*>(&v_lds[buf][wave][0][((lane >> 4) & 1) * 32 + (lane & 15)]) + (lane >> 5);
+    static_for<M>([&](auto J) {
+      constexpr int j = J;
+      const uint32_t c0 = decode2<0>(x.v[j], x.template scale<0, j>());
+      const uint32_t c1 = decode2<1>(x.v[j], x.template scale<1, j>());
+      const uint32_t c2_ = decode2<2>(x.v[j], x.template scale<2, j>());
+      const uint32_t c3 = decode2<3>(x.v[j], x.template scale<3, j>());
+      dst[j * 128] = make_uint2(__builtin_amdgcn_perm(c1, c0, 0x05040100), __builtin_amdgcn_perm(c3, c2_, 0x05040100));
+      dst[j * 128 + 32] = make_uint2(__builtin_amdgcn_perm(c1, c0, 0x07060302), __builtin_amdgcn_perm(c3, c2_, 0x07060302));
+    });
+  };
+
+  float m = kLowest, l = 0.f;
+  v16f o[M];
+#pragma unroll
+  for (int j = 0; j < M; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[j][e] = 0.f;
+
+  if (steps > 0) {
+    load_v(0);
+    load_k(0);
+    decode_v(0, 0);
+    load_v(1);
+  }
+  __syncthreads();
+  for (int st = 0; st < steps; ++st) {
+    const int t = t0 + 64 * st;
+    const bool mine = t < wave_hi && t + 64 > wave_lo;  // else no row of the wave sees any of it
+    v16f s[2];
+    if (mine) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[x][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const v8i kv = {(int)k[x][c].x, (int)k[x][c].y, (int)k[x][c].z, (int)k[x][c].w, 0, 0, 0, 0};
+          s[x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_hi[c], s[x], 4, 0, 0, (int)ks[x][c], 0, (int)q_sc);
+          s[x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_lo[c], s[x], 4, 0, 0, (int)ks[x][c], 0,
+                                                                 (int)(q_sc - 5u));
+        }
+      }
+    }
+    uint32_t hidden = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hidden |= page_at(min(4 * st + i, tiles - 1)) < 0 ? 1u << i : 0u;
+    if (st + 1 < steps) {
+      load_k(st + 1);
+      decode_v(st + 1, (st + 1) & 1);
+      if (((4 * (st + 1)) >> 6) != group) {  // the next step begins the next group of tiles
+        page0 = page1;
+        page1 = pages_of_group(++group + 1);
+      }
+      load_v(st + 2);
+    }
+    if (mine) {
+      if (t < all_lo || t + 64 > all_hi || hidden) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int tok = t + 32 * x + 8 * (e / 4) + 4 * half + e % 4;
+            if (tok < row_lo || tok >= min(row_hi, t1) || ((hidden >> (2 * x + e / 8)) & 1u)) s[x][e] = -INFINITY;
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
+      top *= c2;
+      if (__any(top > m + kLag)) {  // as in the kernel above
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m1 = fmaxf(m, top), alpha = __builtin_amdgcn_exp2f(m - m1);
+        m = m1;
+        l *= alpha;
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[j][e] *= alpha;
+      }
+      uint32_t p[2][8];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const uint32_t u = pack_bf16(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x][e], c2, -m)),
+                                       __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][e + 1], c2, -m)));
+          p[x][e / 2] = u;
+          l = add_pair(l, u);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8 pt = as_bf16x8(p[i / 2][4 * (i % 2)], p[i / 2][4 * (i % 2) + 1], p[i / 2][4 * (i % 2) + 2],
+                                    p[i / 2][4 * (i % 2) + 3]);
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+          const bf16x8 vt = __builtin_bit_cast(bf16x8, v_lds[st & 1][i][j][lane]);
+          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt, pt, o[j], 0, 0, 0);
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  if (32 * wave + col >= w.rows) return;
+  l += __shfl_xor(l, 32);
+  const int t = w.q0 + r / a.G, hq = h * a.G + r % a.G;
+  const float inv = splits > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+  const int64_t at = ((int64_t)split * a.T + t) * a.Hq + hq;
+#pragma unroll
+  for (int j = 0; j < M; ++j)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[2 * e] = o[j][4 * x + e] * inv;
+        f[2 * e + 1] = o[j][8 + 4 * x + e] * inv;
+      }
+      const int d = 32 * j + 16 * x + 8 * half;
+      if (splits == 1) {
+        *reinterpret_cast<uint4*>(a.out + (int64_t)t * a.out_stride + hq * D + d) =
+            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+      } else {
+        *reinterpret_cast<v4f*>(part + at * D + d) = (v4f){f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<v4f*>(part + at * D + d + 4) = (v4f){f[4], f[5], f[6], f[7]};
+      }
+    }
+  if (splits > 1 && half == 0) part_ml[at] = make_float2(m, l);
+}
+
+// How one of the two kernels cuts: rows of a tile, tokens of a split, most splits.
+struct KvSplit {
+  int R, C, S;
+};
+
 // Joins the splits of the rows that were split: one wave per row and query head.
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int R, int rows_least, int rows_most, int C, int S,
+__global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, KvSplit few, KvSplit many, int rows_most,
                                                       const float* __restrict__ part, const float2* __restrict__ part_ml) {
   constexpr int E = D / 64;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -499,12 +773,13 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int R, int r
     lo += (max((int)__popcll(__ballot(at)), 1) - 1) * step;
     hi = min(hi, lo + step);
   }
-  const int q0 = clamp_int(a.cu_q[lo], 0, a.T);
+  const int q0 = clamp_int(a.cu_q[lo], 0, a.T), n = clamp_int(a.cu_q[lo + 1], q0, a.T) - q0;
+  if (t < q0 || t >= q0 + n) return;
+  const KvSplit k = n * a.G <= rows_most ? few : many;
   const int r = (t - q0) * a.G + hq % a.G;
   RowTile w;
-  if (t < q0 || !row_tile_of(a, R, lo, r / R * R, w) || r >= w.n * a.G) return;
-  if (w.n * a.G < rows_least || w.n * a.G > rows_most) return;
-  const int splits = splits_of(w, C, S);
+  if (!row_tile_of(a, k.R, lo, r / k.R * k.R, w)) return;
+  const int splits = splits_of(w, k.C, k.S);
   if (splits == 1) return;  // written already
   const int64_t each = (int64_t)a.T * a.Hq;
   float m = kLowest, l = 0.f, x[E];
@@ -536,57 +811,86 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int R, int r
 
 constexpr int kAllRows = 0x7FFFFFFF;
 
+// Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not
+// launched), the others in the many-rows kernel (rows_most == kAllRows: not launched).
 struct KvPlan {
-  int NT, C, S;
+  int rows_most;
+  KvSplit few, many;
 };
 
-int round_up(int64_t x, int64_t n) { return (int)((x + n - 1) / n * n); }
+size_t part_bytes(const KvAttnSizes& z, int64_t S) { return S <= 1 ? 0 : (size_t)(S * z.T * z.Hq * (z.D + 2) * 4); }
 
-size_t part_bytes(const KvAttnSizes& z, int S) { return S <= 1 ? 0 : (size_t)(S * z.T * z.Hq * (z.D + 2) * 4); }
+// Splits of one kernel: at least `least` tokens each, and no more of them than bring its
+// `groups` workgroups to `wanted`.
+void split_tokens(KvSplit& k, int64_t span, int64_t groups, int64_t wanted, int64_t least, int64_t multiple) {
+  const int64_t S = std::max<int64_t>(1, wanted / std::max<int64_t>(groups, 1));
+  const int64_t C = std::max(least, (span + S - 1) / S);
+  k.C = (int)((C + multiple - 1) / multiple * multiple);
+  k.S = (int)std::max<int64_t>(1, (span + k.C - 1) / k.C);
+}
 
 KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   KvPlan p;
-  const int64_t G = z.Hq / z.H, rows = std::min(z.max_q, z.T) * G;
-  p.NT = rows <= 16 ? 1 : 2;
+  const int64_t G = z.Hq / z.H, max_q = std::min(z.max_q, z.T), rows = max_q * G;
   int64_t span = std::min(z.max_kv, (int64_t)1 << 30);
-  if (z.window) span = std::min(span, z.window + std::min(z.max_q, z.T) + 16);
-  const int64_t R = 16 * p.NT, groups = z.H * std::max(z.B * ((rows + R - 1) / R), z.T * G / R);
-  int64_t S = std::max<int64_t>(1, 1024 / groups);
-  p.C = std::max(256, round_up((span + S - 1) / S, 128));
-  p.S = (int)((span + p.C - 1) / p.C);
-  if (part_bytes(z, p.S) > workspace_bytes) {
-    p.C = 1 << 30;
-    p.S = 1;
+  if (z.window) span = std::min(span, z.window + max_q + 16);
+  p.few.R = rows <= 16 || (rows > 32 && G <= 16) ? 16 : 32;
+  p.many.R = kManyRows;
+  const int64_t few_tiles = z.T * G / p.few.R + z.B;
+  if (rows <= 32 && few_tiles * z.H <= (1 << 20)) p.rows_most = kAllRows;
+  else if (z.T == z.B * max_q || few_tiles * z.H > (1 << 20)) p.rows_most = 0;  // every request has max_q rows
+  else p.rows_most = p.few.R;
+  const int64_t each = rows <= 32 ? (rows + p.few.R - 1) / p.few.R : 1;
+  split_tokens(p.few, span, z.H * std::max(z.B * each, p.rows_most == kAllRows ? z.T * G / p.few.R : 0), 1024, 256, 128);
+  split_tokens(p.many, span, z.H * std::max(z.T * G / kManyRows, (int64_t)1), 512, 512, 64);
+  if (p.rows_most == kAllRows) p.many.S = 1;
+  if (p.rows_most == 0) p.few.S = 1;
+  if (part_bytes(z, std::max(p.few.S, p.many.S)) > workspace_bytes) {
+    p.few.C = p.many.C = 1 << 30;
+    p.few.S = p.many.S = 1;
   }
   return p;
 }
 
 template <int D>
-hipError_t launch_few(const KvAttnArgs& a, const KvAttnSizes& z, const KvPlan& p, void* ws, hipStream_t st) {
+hipError_t launch(const KvAttnArgs& a, const KvAttnSizes& z, const KvPlan& p, void* ws, hipStream_t st) {
+  const int S = std::max(p.few.S, p.many.S);
   float* part = static_cast<float*>(ws);
-  float2* ml = reinterpret_cast<float2*>(part + (size_t)p.S * a.T * a.Hq * D);
-  const unsigned grid = (unsigned)((int64_t)row_tiles(z, 16 * p.NT) * a.H * p.S);
-  if (p.NT == 1)
-    hipLaunchKernelGGL((k_kv_attn_few<D, 1>), dim3(grid), dim3(64 * kFewWaves), 0, st, a, kAllRows, p.C, p.S, part, ml);
-  else
-    hipLaunchKernelGGL((k_kv_attn_few<D, 2>), dim3(grid), dim3(64 * kFewWaves), 0, st, a, kAllRows, p.C, p.S, part, ml);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.S == 1) return e;
-  hipLaunchKernelGGL((k_kv_attn_join<D>), dim3((unsigned)(((int64_t)a.T * a.Hq + 3) / 4)), dim3(256), 0, st, a, 16 * p.NT, 0,
-                     kAllRows, p.C, p.S, (const float*)part, (const float2*)ml);
+  float2* ml = reinterpret_cast<float2*>(part + (size_t)S * a.T * a.Hq * D);
+  if (p.rows_most > 0) {
+    const unsigned grid = (unsigned)((int64_t)row_tiles(z, p.few.R) * a.H * p.few.S);
+    if (p.few.R == 16)
+      hipLaunchKernelGGL((k_kv_attn_few<D, 1>), dim3(grid), dim3(64 * kFewWaves), 0, st, a, p.rows_most, p.few.C, p.few.S, part, ml);
+    else
+      hipLaunchKernelGGL((k_kv_attn_few<D, 2>), dim3(grid), dim3(64 * kFewWaves), 0, st, a, p.rows_most, p.few.C, p.few.S, part, ml);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (p.rows_most < kAllRows) {
+    const unsigned grid = (unsigned)((int64_t)row_tiles(z, kManyRows) * a.H * p.many.S);
+    hipLaunchKernelGGL((k_kv_attn_many<D>), dim3(grid), dim3(64 * kManyWaves), 0, st, a, p.rows_most + 1, p.many.C, p.many.S, part, ml);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (S == 1) return hipSuccess;
+  hipLaunchKernelGGL((k_kv_attn_join<D>), dim3((unsigned)(((int64_t)a.T * a.Hq + 3) / 4)), dim3(256), 0, st, a, p.few, p.many,
+                     p.rows_most, (const float*)part, (const float2*)ml);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t kv_attn_workspace_bytes(const KvAttnSizes& z) { return part_bytes(z, plan_of(z, ~(size_t)0).S); }
+size_t kv_attn_workspace_bytes(const KvAttnSizes& z) {
+  const KvPlan p = plan_of(z, ~(size_t)0);
+  return part_bytes(z, std::max(p.few.S, p.many.S));
+}
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, const KvAttnSizes& z, void* workspace, size_t workspace_bytes,
                           hipStream_t st) {
   const KvPlan p = plan_of(z, workspace_bytes);
-  if (a.D == 64) return launch_few<64>(a, z, p, workspace, st);
-  if (a.D == 128) return launch_few<128>(a, z, p, workspace, st);
-  return launch_few<256>(a, z, p, workspace, st);
+  if (a.D == 64) return launch<64>(a, z, p, workspace, st);
+  if (a.D == 128) return launch<128>(a, z, p, workspace, st);
+  return launch<256>(a, z, p, workspace, st);
 }
 
 void kv_attn_plan(const KvAttnSizes& z, size_t workspace_bytes, char* buf, size_t len) {
@@ -595,7 +899,13 @@ void kv_attn_plan(const KvAttnSizes& z, size_t workspace_bytes, char* buf, size_
     return;
   }
   const KvPlan p = plan_of(z, workspace_bytes);
-  std::snprintf(buf, len, "k_kv_attn_few<%d, %d> C=%d S=%d%s", (int)z.D, p.NT, p.C, p.S, p.S > 1 ? " + k_kv_attn_join" : "");
+  char few[64] = "", many[64] = "";
+  if (p.rows_most > 0)
+    std::snprintf(few, sizeof few, "k_kv_attn_few<%d, %d> C=%d S=%d", (int)z.D, p.few.R / 16, p.few.C, p.few.S);
+  if (p.rows_most < kAllRows)
+    std::snprintf(many, sizeof many, "k_kv_attn_many<%d> C=%d S=%d", (int)z.D, p.many.C, p.many.S);
+  std::snprintf(buf, len, "%s%s%s%s", few, few[0] && many[0] ? " + " : "", many,
+                p.few.S > 1 || p.many.S > 1 ? " + k_kv_attn_join" : "");
 }
 
 }  // namespace mx

@@ -214,18 +214,41 @@ struct TokenTile {  // one lane's share of 16 tokens
 };
 
 constexpr int kFewWaves = 4;
+constexpr int kAllRows = 0x7FFFFFFF;
+
+// How a kernel cuts: rows of a tile, tokens of a split, most splits.
+struct KvSplit {
+  int R, C, S;
+};
+// Partial results of split rows in the workspace: unscaled sums o [S][T][Hq][D] with their maximum
+// and sum of weights ml [S][T][Hq], and in how many splits a row is, count [T][Hq] (1: the row is
+// in the output already). All null where nothing is split.
+struct KvParts {
+  float* o;
+  float2* ml;
+  int32_t* count;
+  __device__ __forceinline__ int64_t at(const KvAttnArgs& a, int split, int t, int hq) const {
+    return ((int64_t)split * a.T + t) * a.Hq + hq;
+  }
+};
+
+// Waves a SIMD that the registers allow without spilling.
+constexpr int few_occupancy(int D, int NT) { return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 3 : 2) : 1; }
 
 template <int D, int NT>
-__global__ __launch_bounds__(64 * kFewWaves) void k_kv_attn_few(KvAttnArgs a, int rows_most, int C, int S,
-                                                                float* __restrict__ part, float2* __restrict__ part_ml) {
+__global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_attn_few(KvAttnArgs a, int rows_most,
+                                                                                      KvSplit k, KvParts out) {
   constexpr int R = 16 * NT, M = D / 32, KC = (D + 127) / 128, LD = D + 4;
   __shared__ float o_all[kFewWaves][16][LD];
   __shared__ float2 ml_all[kFewWaves][R];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
-  const int split = (int)(blockIdx.x % S), h = (int)(blockIdx.x / S % a.H);
+  const int C = k.C, S = k.S, split = (int)(blockIdx.x % S), h = (int)(blockIdx.x / S % a.H), tile = (int)(blockIdx.x / S / a.H);
   RowTile w;
-  if (!find_row_tile(a, R, (int)(blockIdx.x / S / a.H), w)) return;
-  if (w.n * a.G > rows_most) return;  // the other kernel's
+  if (rows_most == kAllRows) {
+    if (!find_row_tile(a, R, tile, w)) return;
+  } else if (!row_tile_of(a, R, tile, 0, w) || w.n * a.G > rows_most) {  // a tile a request; larger ones are
+    return;                                                              // the other kernel's
+  }
   const int splits = splits_of(w, C, S);
   if (split >= splits) return;
 
@@ -478,11 +501,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_attn_few(KvAttnArgs a, in
       for (int e = 0; e < E; e += 4)
         *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16(x[e] * inv, x[e + 1] * inv), pack_bf16(x[e + 2] * inv, x[e + 3] * inv));
     } else {
-      const int64_t at = ((int64_t)split * a.T + t) * a.Hq + hq;
+      float* dst = out.o + out.at(a, split, t, hq) * D + d0;
 #pragma unroll
-      for (int e = 0; e < E; e += 4) *reinterpret_cast<v4f*>(part + at * D + d0 + e) = (v4f){x[e], x[e + 1], x[e + 2], x[e + 3]};
-      if (threadIdx.x % 16 == 0) part_ml[at] = make_float2(M1, L);
+      for (int e = 0; e < E; e += 4) *reinterpret_cast<v4f*>(dst + e) = (v4f){x[e], x[e + 1], x[e + 2], x[e + 3]};
+      if (threadIdx.x % 16 == 0) out.ml[out.at(a, split, t, hq)] = make_float2(M1, L);
     }
+    if (split == 0 && out.count && threadIdx.x % 16 == 0) out.count[out.at(a, 0, t, hq)] = splits;
   }
 }
 
@@ -501,12 +525,12 @@ constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 template <int D>
-__global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_many(KvAttnArgs a, int rows_least, int C, int S,
-                                                                  float* __restrict__ part, float2* __restrict__ part_ml) {
+__global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_many(KvAttnArgs a, int rows_least,
+                                                                                              KvSplit cut, KvParts out) {
   constexpr int M = D / 32, KC = D / 64;
   __shared__ uint4 v_lds[2][4][M][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, half = lane >> 5;
-  const int split = (int)(blockIdx.x % S), h = (int)(blockIdx.x / S % a.H);
+  const int C = cut.C, S = cut.S, split = (int)(blockIdx.x % S), h = (int)(blockIdx.x / S % a.H);
   RowTile w;
   // last tiles first: with a causal mask they see the most tokens
   if (!find_row_tile(a, kManyRows, (int)(gridDim.x / S / a.H - 1 - blockIdx.x / S / a.H), w)) return;
@@ -729,7 +753,7 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
   l += __shfl_xor(l, 32);
   const int t = w.q0 + r / a.G, hq = h * a.G + r % a.G;
   const float inv = splits > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
-  const int64_t at = ((int64_t)split * a.T + t) * a.Hq + hq;
+  const int64_t at = out.at(a, split, t, hq);
 #pragma unroll
   for (int j = 0; j < M; ++j)
 #pragma unroll
@@ -745,57 +769,55 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
         *reinterpret_cast<uint4*>(a.out + (int64_t)t * a.out_stride + hq * D + d) =
             make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
       } else {
-        *reinterpret_cast<v4f*>(part + at * D + d) = (v4f){f[0], f[1], f[2], f[3]};
-        *reinterpret_cast<v4f*>(part + at * D + d + 4) = (v4f){f[4], f[5], f[6], f[7]};
+        *reinterpret_cast<v4f*>(out.o + at * D + d) = (v4f){f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<v4f*>(out.o + at * D + d + 4) = (v4f){f[4], f[5], f[6], f[7]};
       }
     }
-  if (splits > 1 && half == 0) part_ml[at] = make_float2(m, l);
+  if (splits > 1 && half == 0) out.ml[at] = make_float2(m, l);
+  if (split == 0 && out.count && half == 0) out.count[at] = splits;
 }
 
-// How one of the two kernels cuts: rows of a tile, tokens of a split, most splits.
-struct KvSplit {
-  int R, C, S;
-};
-
-// Joins the splits of the rows that were split: one wave per row and query head.
-template <int D>
-__global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, KvSplit few, KvSplit many, int rows_most,
-                                                      const float* __restrict__ part, const float2* __restrict__ part_ml) {
+// Joins the splits: W waves (1 or 4) per row and query head, each every W-th split, added in a
+// fixed order. Which rows are split, and in how many, is read with the maxima: two dependent
+// loads to the first sums.
+template <int D, int W>
+__global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvParts in) {
   constexpr int E = D / 64;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= (int64_t)a.T * a.Hq) return;
+  __shared__ float o_all[4][D];
+  __shared__ float l_all[4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, part = W == 1 ? 0 : wave;
+  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x, each = (int64_t)a.T * a.Hq;
+  if (row >= each) return;
   const int t = (int)(row / a.Hq), hq = (int)(row % a.Hq);
-  int lo = 0, hi = a.B;  // the request of row t
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 63) / 64, b = lo + lane * step;
-    const bool at = b < hi && a.cu_q[b] <= t;
-    lo += (max((int)__popcll(__ballot(at)), 1) - 1) * step;
-    hi = min(hi, lo + step);
-  }
-  const int q0 = clamp_int(a.cu_q[lo], 0, a.T), n = clamp_int(a.cu_q[lo + 1], q0, a.T) - q0;
-  if (t < q0 || t >= q0 + n) return;
-  const KvSplit k = n * a.G <= rows_most ? few : many;
-  const int r = (t - q0) * a.G + hq % a.G;
-  RowTile w;
-  if (!row_tile_of(a, k.R, lo, r / k.R * k.R, w)) return;
-  const int splits = splits_of(w, k.C, k.S);
-  if (splits == 1) return;  // written already
-  const int64_t each = (int64_t)a.T * a.Hq;
+  if (t < a.cu_q[0] || t >= a.cu_q[a.B]) return;  // no request's
+  const int splits = min(in.count[row], S);
+  if (splits <= 1) return;  // written already
   float m = kLowest, l = 0.f, x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = 0.f;
-  for (int s = lane; s < splits; s += 64) m = fmaxf(m, part_ml[s * each + row].x);
+  for (int s = lane; s < splits; s += 64) m = fmaxf(m, in.ml[s * each + row].x);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float2 ml = part_ml[s * each + row];
+  typedef float vec __attribute__((ext_vector_type(E)));
+#pragma unroll 8
+  for (int s = part; s < splits; s += W) {
+    const float2 ml = in.ml[s * each + row];
+    const vec y = *reinterpret_cast<const vec*>(in.o + (s * each + row) * D + lane * E);
     const float f = __builtin_amdgcn_exp2f(ml.x - m);
     l += ml.y * f;
-    const float* src = part + (s * each + row) * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] += src[e] * f;
+    for (int e = 0; e < E; ++e) x[e] += y[e] * f;
+  }
+  if constexpr (W == 4) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) o_all[wave][lane * E + e] = x[e];
+    if (lane == 0) l_all[wave] = l;
+    __syncthreads();
+    if (wave != 0) return;
+    l = ((l_all[0] + l_all[1]) + l_all[2]) + l_all[3];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      x[e] = ((o_all[0][lane * E + e] + o_all[1][lane * E + e]) + o_all[2][lane * E + e]) + o_all[3][lane * E + e];
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint16_t* dst = a.out + (int64_t)t * a.out_stride + hq * D + lane * E;
@@ -809,8 +831,6 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, KvSplit few,
 
 // ------------------------------------------------------------------------------- the launch
 
-constexpr int kAllRows = 0x7FFFFFFF;
-
 // Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not
 // launched), the others in the many-rows kernel (rows_most == kAllRows: not launched).
 struct KvPlan {
@@ -818,12 +838,16 @@ struct KvPlan {
   KvSplit few, many;
 };
 
-size_t part_bytes(const KvAttnSizes& z, int64_t S) { return S <= 1 ? 0 : (size_t)(S * z.T * z.Hq * (z.D + 2) * 4); }
+size_t part_bytes(const KvAttnSizes& z, int64_t S) {
+  return S <= 1 ? 0 : (size_t)(z.T * z.Hq * (S * (z.D + 2) + 1) * 4);
+}
 
-// Splits of one kernel: at least `least` tokens each, and no more of them than bring its
-// `groups` workgroups to `wanted`.
-void split_tokens(KvSplit& k, int64_t span, int64_t groups, int64_t wanted, int64_t least, int64_t multiple) {
-  const int64_t S = std::max<int64_t>(1, wanted / std::max<int64_t>(groups, 1));
+// Splits of one kernel whose row tiles see `span` tokens at most: enough of them that `groups`
+// busy workgroups become `wanted`, at least `least` tokens each. launched: row tiles and heads of
+// the launch, of which many may have nothing to do.
+void split_tokens(KvSplit& k, int64_t span, int64_t groups, int64_t launched, int64_t wanted, int64_t least,
+                  int64_t multiple) {
+  const int64_t S = std::max<int64_t>(1, std::min(wanted / std::max<int64_t>(groups, 1), ((int64_t)1 << 20) / launched));
   const int64_t C = std::max(least, (span + S - 1) / S);
   k.C = (int)((C + multiple - 1) / multiple * multiple);
   k.S = (int)std::max<int64_t>(1, (span + k.C - 1) / k.C);
@@ -831,18 +855,19 @@ void split_tokens(KvSplit& k, int64_t span, int64_t groups, int64_t wanted, int6
 
 KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   KvPlan p;
-  const int64_t G = z.Hq / z.H, max_q = std::min(z.max_q, z.T), rows = max_q * G;
-  int64_t span = std::min(z.max_kv, (int64_t)1 << 30);
-  if (z.window) span = std::min(span, z.window + max_q + 16);
-  p.few.R = rows <= 16 || (rows > 32 && G <= 16) ? 16 : 32;
+  const int64_t G = z.Hq / z.H, max_q = std::min(z.max_q, z.T), rows = max_q * G, few_rows = z.D == 256 ? 16 : 32;
+  p.few.R = rows <= 16 || (rows > few_rows && G <= 16) || z.D == 256 ? 16 : 32;
   p.many.R = kManyRows;
-  const int64_t few_tiles = z.T * G / p.few.R + z.B;
-  if (rows <= 32 && few_tiles * z.H <= (1 << 20)) p.rows_most = kAllRows;
-  else if (z.T == z.B * max_q || few_tiles * z.H > (1 << 20)) p.rows_most = 0;  // every request has max_q rows
+  const bool few_fit = (z.T * G / p.few.R + z.B) * z.H <= (1 << 20);
+  if (rows <= few_rows && few_fit) p.rows_most = kAllRows;
+  else if (z.T == z.B * max_q || !few_fit) p.rows_most = 0;  // every request has max_q rows
   else p.rows_most = p.few.R;
-  const int64_t each = rows <= 32 ? (rows + p.few.R - 1) / p.few.R : 1;
-  split_tokens(p.few, span, z.H * std::max(z.B * each, p.rows_most == kAllRows ? z.T * G / p.few.R : 0), 1024, 256, 128);
-  split_tokens(p.many, span, z.H * std::max(z.T * G / kManyRows, (int64_t)1), 512, 512, 64);
+  const int64_t longest = std::min(z.max_kv, (int64_t)1 << 30);
+  auto span = [&](int R) { return z.window ? std::min(longest, z.window + R / G + 16) : longest; };
+  const int64_t few_tiles = p.rows_most == kAllRows ? std::max(z.B * ((rows + p.few.R - 1) / p.few.R), z.T * G / p.few.R) : z.B;
+  split_tokens(p.few, span(p.few.R), z.H * few_tiles, z.H * (z.T * G / p.few.R + z.B), 2048, 256, 128);
+  split_tokens(p.many, span(p.many.R), z.H * std::max<int64_t>(z.T * G / kManyRows, 1), z.H * row_tiles(z, kManyRows), 2048,
+               512, 64);
   if (p.rows_most == kAllRows) p.many.S = 1;
   if (p.rows_most == 0) p.few.S = 1;
   if (part_bytes(z, std::max(p.few.S, p.many.S)) > workspace_bytes) {
@@ -855,26 +880,32 @@ KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
 template <int D>
 hipError_t launch(const KvAttnArgs& a, const KvAttnSizes& z, const KvPlan& p, void* ws, hipStream_t st) {
   const int S = std::max(p.few.S, p.many.S);
-  float* part = static_cast<float*>(ws);
-  float2* ml = reinterpret_cast<float2*>(part + (size_t)S * a.T * a.Hq * D);
+  const size_t each = (size_t)a.T * a.Hq;
+  KvParts parts = {nullptr, nullptr, nullptr};
+  if (S > 1) {
+    parts.o = static_cast<float*>(ws);
+    parts.ml = reinterpret_cast<float2*>(parts.o + S * each * D);
+    parts.count = reinterpret_cast<int32_t*>(parts.ml + S * each);
+  }
+  hipError_t e = hipSuccess;
   if (p.rows_most > 0) {
-    const unsigned grid = (unsigned)((int64_t)row_tiles(z, p.few.R) * a.H * p.few.S);
-    if (p.few.R == 16)
-      hipLaunchKernelGGL((k_kv_attn_few<D, 1>), dim3(grid), dim3(64 * kFewWaves), 0, st, a, p.rows_most, p.few.C, p.few.S, part, ml);
-    else
-      hipLaunchKernelGGL((k_kv_attn_few<D, 2>), dim3(grid), dim3(64 * kFewWaves), 0, st, a, p.rows_most, p.few.C, p.few.S, part, ml);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    const int64_t tiles = p.rows_most == kAllRows ? row_tiles(z, p.few.R) : z.B;
+    const dim3 grid((unsigned)(tiles * a.H * p.few.S)), block(64 * kFewWaves);
+    if (D == 256 || p.few.R == 16) hipLaunchKernelGGL((k_kv_attn_few<D, 1>), grid, block, 0, st, a, p.rows_most, p.few, parts);
+    else hipLaunchKernelGGL((k_kv_attn_few<D == 256 ? 64 : D, 2>), grid, block, 0, st, a, p.rows_most, p.few, parts);
+    e = hipGetLastError();
   }
-  if (p.rows_most < kAllRows) {
-    const unsigned grid = (unsigned)((int64_t)row_tiles(z, kManyRows) * a.H * p.many.S);
-    hipLaunchKernelGGL((k_kv_attn_many<D>), dim3(grid), dim3(64 * kManyWaves), 0, st, a, p.rows_most + 1, p.many.C, p.many.S, part, ml);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  if (e == hipSuccess && p.rows_most < kAllRows) {
+    const dim3 grid((unsigned)((int64_t)row_tiles(z, kManyRows) * a.H * p.many.S)), block(64 * kManyWaves);
+    hipLaunchKernelGGL((k_kv_attn_many<D>), grid, block, 0, st, a, p.rows_most + 1, p.many, parts);
+    e = hipGetLastError();
   }
-  if (S == 1) return hipSuccess;
-  hipLaunchKernelGGL((k_kv_attn_join<D>), dim3((unsigned)(((int64_t)a.T * a.Hq + 3) / 4)), dim3(256), 0, st, a, p.few, p.many,
-                     p.rows_most, (const float*)part, (const float2*)ml);
+  if (e != hipSuccess || S == 1) return e;
+  // four waves a row where there are many splits to add and few rows to fill the chip
+  if (S > 8 && each <= 4096)
+    hipLaunchKernelGGL((k_kv_attn_join<D, 4>), dim3((unsigned)each), dim3(256), 0, st, a, S, parts);
+  else
+    hipLaunchKernelGGL((k_kv_attn_join<D, 1>), dim3((unsigned)((each + 3) / 4)), dim3(256), 0, st, a, S, parts);
   return hipGetLastError();
 }
 

@@ -143,17 +143,27 @@ template <int I>
 __device__ __forceinline__ uint32_t decode2(uint32_t codes, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, I));
 }
+// Byte J of a word as the exponent of an FP32 scale, in one instruction (the compiler's own form
+// for bytes 0 to 2 is a shift and a mask); shift: 23 in a register.
 template <int J>
-__device__ __forceinline__ float scale_at(uint32_t w) {
-  if constexpr (J == 3) return __builtin_bit_cast(float, (w >> 1) & 0x7F800000u);
-  return __builtin_bit_cast(float, ((w >> (8 * J)) & 0xFFu) << 23);
+__device__ __forceinline__ float scale_at(uint32_t w, uint32_t shift) {
+  uint32_t r;
+  if constexpr (J == 0)
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0" : "=v"(r) : "v"(shift), "v"(w));
+  else if constexpr (J == 1)
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1" : "=v"(r) : "v"(shift), "v"(w));
+  else if constexpr (J == 2)
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2" : "=v"(r) : "v"(shift), "v"(w));
+  else
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3" : "=v"(r) : "v"(shift), "v"(w));
+  return __builtin_bit_cast(float, r);
 }
 
 // ------------------------------------------------------------------------------- few rows
 //
 // Decoding and drafts: one workgroup of four waves takes a tile of 16 NT rows and C tokens of one
-// head, each wave a quarter of them on its own, 32 tokens a step, the next step's operands in
-// flight. The transposed products put a query row in each of the 16 columns:
+// head, each wave a quarter of them on its own, 32 tokens a step; the next step's keys are fetched
+// when this step's are in the products, its values likewise. The transposed products put a query row in each of the 16 columns:
 //   S^T (16 tokens x 16 rows) = K Q^T    scaled 16x16x128 MFMA, A = K codes from the cache,
 //   O^T (D x 16 rows)        += V^T P^T  bf16 16x16x32 MFMA, A = V decoded in registers.
 // A lane's four scores of each of two token tiles (tokens 4g..4g+3) are, rounded to bf16, its
@@ -170,24 +180,26 @@ struct TokenTile {  // one lane's share of 16 tokens
   uint32_t v[M];   // word j: the lane's element pair of scale block j, four tokens
   uint32_t vs[M];  // the 4 M scale bytes of its four tokens
 
-  __device__ __forceinline__ void load(const uint8_t* blk, int P, int in_page, int lane) {
-    const int g = lane >> 4;
+  __device__ __forceinline__ void load_k(const uint8_t* blk, int P, int in_page, uint32_t lane) {
     const uint8_t* kc = blk + in_page * (8 * D);
     const uint8_t* kb = blk + P * D + in_page * (D / 2);
     if constexpr (D == 64) {
-      k[0] = *reinterpret_cast<const u32x4*>(kc + (lane & 31) * 16);
-      ks[0] = kb[lane & 31];
+      k[0] = *reinterpret_cast<const u32x4*>(kc + (lane & 31u) * 16u);
+      ks[0] = kb[lane & 31u];
     } else {
 #pragma unroll
       for (int c = 0; c < D / 128; ++c) {
-        k[c] = *reinterpret_cast<const u32x4*>(kc + c * 1024 + lane * 16);
-        ks[c] = kb[c * 64 + lane];
+        k[c] = *reinterpret_cast<const u32x4*>(kc + (c * 1024u + lane * 16u));
+        ks[c] = kb[c * 64u + lane];
       }
     }
-    const uint8_t* vc = blk + P * (D / 2) + in_page * (8 * D) + lane * (4 * M);
-    const uint8_t* vb = blk + P * D + P * M + in_page * (16 * M) + g * (4 * M);
+  }
+  __device__ __forceinline__ void load_v(const uint8_t* blk, int P, int in_page, uint32_t lane) {
+    const uint8_t* vc = blk + P * (D / 2) + in_page * (8 * D);
+    const uint8_t* vb = blk + P * D + P * M + in_page * (16 * M);
     typedef uint32_t words __attribute__((ext_vector_type(M)));
-    const words a = *reinterpret_cast<const words*>(vc), b = *reinterpret_cast<const words*>(vb);
+    const words a = *reinterpret_cast<const words*>(vc + lane * (4u * M));
+    const words b = *reinterpret_cast<const words*>(vb + (lane >> 4) * (4u * M));
 #pragma unroll
     for (int j = 0; j < M; ++j) {
       v[j] = a[j];
@@ -196,8 +208,8 @@ struct TokenTile {  // one lane's share of 16 tokens
   }
   // Scale of block j of the lane's token i: byte (i M + j) of vs.
   template <int I, int J>
-  __device__ __forceinline__ float scale() const {
-    return scale_at<(I * M + J) % 4>(vs[(I * M + J) / 4]);
+  __device__ __forceinline__ float scale(uint32_t shift) const {
+    return scale_at<(I * M + J) % 4>(vs[(I * M + J) / 4], shift);
   }
   // Scales of the tokens outside [lo, hi) become 0 (2^-127): their codes, never written or
   // written by another request, cannot be infinite then. t: the lane's first token.
@@ -233,7 +245,7 @@ struct KvParts {
 };
 
 // Waves a SIMD that the registers allow without spilling.
-constexpr int few_occupancy(int D, int NT) { return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 3 : 2) : 1; }
+constexpr int few_occupancy(int D, int NT) { return D == 64 ? (NT == 1 ? 5 : 3) : D == 128 ? (NT == 1 ? 4 : 2) : 2; }
 
 template <int D, int NT>
 __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_attn_few(KvAttnArgs a, int rows_most,
@@ -325,6 +337,8 @@ __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_att
   // a step inside [all_lo, all_hi) needs no mask
   const int all_lo = row_begin(a, w.pos(w.rb + w.rows - 1, a.G)), all_hi = min(w1, row_end(a, w.len, w.pos(w.rb, a.G)));
   const float c2 = a.scale * kLog2e;
+  uint32_t shift = 23;
+  asm volatile("" : "+v"(shift));  // kept in a register: scale_at
   const int P = 1 << a.log2_page;
   const int32_t* table = a.block_table + (int64_t)w.b * a.max_blocks;
 
@@ -348,16 +362,31 @@ __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_att
       if (bad) page = 0;
     }
     const uint64_t bad_tiles = __ballot(bad);
-    auto load = [&](TokenTile<D>(&x)[2], int step) {
+    auto block_of = [&](int tile, int& in_page) {
+      in_page = ((base + 16 * tile) & (P - 1)) >> 4;
+      return a.cache + ((int64_t)__builtin_amdgcn_readlane(page, tile) * a.H + h) * a.block_bytes;
+    };
+    TokenTile<D> x[2];
+    auto load_k = [&](int step) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int tile = min(2 * step + i, tiles - 1);
-        const int id = __builtin_amdgcn_readlane(page, tile);
-        const uint8_t* blk = a.cache + ((int64_t)id * a.H + h) * a.block_bytes;
-        x[i].load(blk, P, ((base + 16 * tile) & (P - 1)) >> 4, lane);
+        int in_page;
+        const uint8_t* blk = block_of(min(2 * step + i, tiles - 1), in_page);
+        x[i].load_k(blk, P, in_page, lane);
       }
     };
-    auto compute = [&](TokenTile<D>(&x)[2], int step) {
+    auto load_v = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int in_page;
+        const uint8_t* blk = block_of(min(2 * step + i, tiles - 1), in_page);
+        x[i].load_v(blk, P, in_page, lane);
+      }
+    };
+    const int steps = (tiles + 1) >> 1;
+    load_k(0);
+    load_v(0);
+    for (int step = 0; step < steps; ++step) {
       const int t = base + 32 * step;
       v4f s[NT][2];
 #pragma unroll
@@ -375,6 +404,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_att
                                                                           (int)x[i].ks[c], 0, (int)(q_sc[nt] - 5u));
           }
         }
+      load_k(min(step + 1, steps - 1));  // the last step's loads, of what it has already, go unused
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -427,10 +457,10 @@ __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_att
         uint32_t even[4], odd[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t c0 = decode2<0>(x[i].v[j], x[i].template scale<0, j>());
-          const uint32_t c1 = decode2<1>(x[i].v[j], x[i].template scale<1, j>());
-          const uint32_t c2_ = decode2<2>(x[i].v[j], x[i].template scale<2, j>());
-          const uint32_t c3 = decode2<3>(x[i].v[j], x[i].template scale<3, j>());
+          const uint32_t c0 = decode2<0>(x[i].v[j], x[i].template scale<0, j>(shift));
+          const uint32_t c1 = decode2<1>(x[i].v[j], x[i].template scale<1, j>(shift));
+          const uint32_t c2_ = decode2<2>(x[i].v[j], x[i].template scale<2, j>(shift));
+          const uint32_t c3 = decode2<3>(x[i].v[j], x[i].template scale<3, j>(shift));
           even[2 * i] = __builtin_amdgcn_perm(c1, c0, 0x05040100);
           even[2 * i + 1] = __builtin_amdgcn_perm(c3, c2_, 0x05040100);
           odd[2 * i] = __builtin_amdgcn_perm(c1, c0, 0x07060302);
@@ -444,16 +474,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_att
           o[nt][2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vo, pt, o[nt][2 * j + 1], 0, 0, 0);
         }
       });
-    };
-    const int steps = (tiles + 1) >> 1;
-    TokenTile<D> x0[2], x1[2];
-    load(x0, 0);
-    for (int st = 0; st < steps; st += 2) {
-      load(x1, min(st + 1, steps - 1));
-      compute(x0, st);
-      if (st + 1 >= steps) break;
-      load(x0, min(st + 2, steps - 1));
-      compute(x1, st + 1);
+      load_v(min(step + 1, steps - 1));
     }
   }
 
@@ -583,6 +604,8 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
   const int wave_hi = wave_rows > 0 ? row_end(a, w.len, w.pos(last, a.G)) : 0;
   const int all_lo = row_begin(a, w.pos(last, a.G)), all_hi = min(t1, row_end(a, w.len, w.pos(first, a.G)));
   const float c2 = a.scale * kLog2e;
+  uint32_t shift = 23;
+  asm volatile("" : "+v"(shift));  // kept in a register: scale_at
   const int P = 1 << a.log2_page;
   const int32_t* table = a.block_table + (int64_t)w.b * a.max_blocks;
 
@@ -646,10 +669,10 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
     uint2* dst = reinterpret_cast<uint2*>(&v_lds[buf][wave][0][((lane >> 4) & 1) * 32 + (lane & 15)]) + (lane >> 5);
     static_for<M>([&](auto J) {
       constexpr int j = J;
-      const uint32_t c0 = decode2<0>(x.v[j], x.template scale<0, j>());
-      const uint32_t c1 = decode2<1>(x.v[j], x.template scale<1, j>());
-      const uint32_t c2_ = decode2<2>(x.v[j], x.template scale<2, j>());
-      const uint32_t c3 = decode2<3>(x.v[j], x.template scale<3, j>());
+      const uint32_t c0 = decode2<0>(x.v[j], x.template scale<0, j>(shift));
+      const uint32_t c1 = decode2<1>(x.v[j], x.template scale<1, j>(shift));
+      const uint32_t c2_ = decode2<2>(x.v[j], x.template scale<2, j>(shift));
+      const uint32_t c3 = decode2<3>(x.v[j], x.template scale<3, j>(shift));
       dst[j * 128] = make_uint2(__builtin_amdgcn_perm(c1, c0, 0x05040100), __builtin_amdgcn_perm(c3, c2_, 0x05040100));
       dst[j * 128 + 32] = make_uint2(__builtin_amdgcn_perm(c1, c0, 0x07060302), __builtin_amdgcn_perm(c3, c2_, 0x07060302));
     });

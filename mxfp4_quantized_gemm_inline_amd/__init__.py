@@ -9,6 +9,7 @@ is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -107,8 +108,14 @@ def _torch():
 
 def _stream_ptr(stream=None) -> int:
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    if stream is None:
+        # the handle alone where this torch gives it: its Stream object costs more than a small
+        # call's checks together (2.7 against 0.1 us)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return int(raw(torch.cuda.current_device()))
+        stream = torch.cuda.current_stream()
+    return int(stream.cuda_stream)
 
 
 def _need(t, name, dtype=None, shape=None, min_bytes=None, min_numel=None):
@@ -433,27 +440,45 @@ def mx_kv_cache_bytes(num_pages: int, page_size: int, heads: int, D: int) -> int
     return int(lib().mx_kv_cache_bytes(int(num_pages), int(page_size), int(heads), int(D)))
 
 
-def _kv_pages(cache, page_size, heads, D):
-    """Pages that fit the uint8 buffer `cache`."""
-    torch = _torch()
-    _need(cache, "cache", torch.uint8)
+@functools.lru_cache(maxsize=1024)
+def _kv_page_bytes(page_size: int, heads: int, D: int) -> int:
     per = mx_kv_cache_bytes(1, page_size, heads, D)
     if per == 0:
         raise MxError(MX_ERR_SHAPE, f"kv cache with page_size={page_size}, heads={heads}, D={D}")
+    return per
+
+
+def _kv_pages(cache, page_size, heads, D):
+    """Pages that fit the uint8 buffer `cache`."""
+    _meta(cache, "cache", _torch().uint8)
+    per = _kv_page_bytes(int(page_size), int(heads), int(D))
     pages = cache.numel() // per
     if pages < 1:
         raise ValueError(f"cache holds {cache.numel()} bytes, one page needs {per}")
     return pages
 
 
-def _new(shape, dtype, device, stream):
+def _new(shape, dtype, like, stream):
     """A new tensor of the stream that the call runs on, so that torch neither hands out memory
     the current stream still uses nor reuses it under a kernel of `stream`."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _meta(t, name, dtype, least=0):
+    """The checks of _need that the cache calls use, once per tensor: a decoding step makes a few
+    of these calls per layer, with up to ten tensors each."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() < least:
+        raise ValueError(f"{name} holds {t.numel()} elements, needs at least {least}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _rows3(t, name):
@@ -462,26 +487,36 @@ def _rows3(t, name):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D, got shape {tuple(t.shape)}")
-    T, H, D = (int(d) for d in t.shape)
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    (T, H, D), (row, head, one) = t.shape, t.stride()
+    if (D > 1 and one != 1) or (H > 1 and head != D):
         raise ValueError(f"{name} must have dense rows, got strides {t.stride()}")
-    return T, H, D, int(t.stride(0)) if T > 1 else H * D
+    return T, H, D, row if T > 1 else H * D
 
 
-def _here(t, name):
-    """Device pointer of a tensor checked by _rows3."""
-    torch = _torch()
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.device.index is not None and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
-    return t.data_ptr()
+def _pointers(**tensors):
+    """Device pointers of tensors whose metadata was checked (None stays None): all of them on
+    the current device."""
+    current, out = None, []
+    for name, t in tensors.items():
+        if t is None:
+            out.append(None)
+            continue
+        index = t.get_device()
+        if index < 0:
+            raise ValueError(f"{name} must be a device tensor")
+        if current is None:
+            current = _torch().cuda.current_device()
+        if index != current:
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{current}")
+        out.append(t.data_ptr())
+    return out
 
 
+@functools.lru_cache(maxsize=1024)
 def mx_kv_tables_workspace_bytes(B: int, max_rows: int) -> int:
     return int(lib().mx_kv_tables_workspace_bytes(int(B), int(max_rows)))
 
@@ -494,75 +529,85 @@ def mx_kv_tables(old_lens, new_lens, block_table, free_pages, free_count, page_s
     free_count_out int32 [1], status int32 [1]); status 0 means done (see mx.h for the rest)."""
     torch = _torch()
     i32 = torch.int32
-    _need(block_table, "block_table", i32)
+    _meta(block_table, "block_table", i32)
     B, max_blocks = _dims2(block_table, "block_table")
-    _need(old_lens, "old_lens", i32, shape=(B,))
-    _need(new_lens, "new_lens", i32, shape=(B,))
-    _need(free_pages, "free_pages", i32)
-    _need(free_count, "free_count", i32, min_numel=1)
-    dev = block_table.device
+    for t, name in ((old_lens, "old_lens"), (new_lens, "new_lens")):
+        _meta(t, name, i32)
+        if t.shape != (B,):
+            raise ValueError(f"{name} must have shape {(B,)}, got {tuple(t.shape)}")
+    _meta(free_pages, "free_pages", i32)
+    _meta(free_count, "free_count", i32, 1)
     max_rows = int(max_rows)
-    cu_q = cu_q if cu_q is not None else _new((B + 1,), i32, dev, stream)
-    slots = slots if slots is not None else _new((max(max_rows, 0),), torch.int64, dev, stream)
-    positions = positions if positions is not None else _new((max(max_rows, 0),), i32, dev, stream)
-    free_count_out = free_count_out if free_count_out is not None else _new((1,), i32, dev, stream)
-    status = status if status is not None else _new((1,), i32, dev, stream)
-    _need(cu_q, "cu_q", i32, min_numel=B + 1)
-    _need(slots, "slots", torch.int64, min_numel=max_rows)
-    _need(positions, "positions", i32, min_numel=max_rows)
-    _need(free_count_out, "free_count_out", i32, min_numel=1)
-    _need(status, "status", i32, min_numel=1)
-    nbytes = mx_kv_tables_workspace_bytes(B, max_rows)
-    if nbytes and workspace is None:
-        workspace = _new((nbytes,), torch.uint8, dev, stream)
-    ws_ptr, ws_bytes = (None, 0)
+    rows = max(max_rows, 0)
+    if cu_q is None and positions is None and free_count_out is None and status is None:
+        cu_q, positions, free_count_out, status = _new((B + rows + 3,), i32, block_table, stream).split((B + 1, rows, 1, 1))
+    else:
+        cu_q = cu_q if cu_q is not None else _new((B + 1,), i32, block_table, stream)
+        positions = positions if positions is not None else _new((rows,), i32, block_table, stream)
+        free_count_out = free_count_out if free_count_out is not None else _new((1,), i32, block_table, stream)
+        status = status if status is not None else _new((1,), i32, block_table, stream)
+        _meta(cu_q, "cu_q", i32, B + 1)
+        _meta(positions, "positions", i32, max_rows)
+        _meta(free_count_out, "free_count_out", i32, 1)
+        _meta(status, "status", i32, 1)
+    if slots is None:
+        slots = _new((rows,), torch.int64, block_table, stream)
+    else:
+        _meta(slots, "slots", torch.int64, max_rows)
+    nbytes, ws_bytes = mx_kv_tables_workspace_bytes(B, max_rows), 0
     if nbytes:
-        ws_ptr, ws_bytes = _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size()
-    _check(lib().mx_kv_tables(
-        _dev(old_lens, i32, "old_lens"), _dev(new_lens, i32, "new_lens"), B, int(page_size),
-        _dev(block_table, i32, "block_table"), max_blocks, _dev(free_pages, i32, "free_pages"), free_pages.numel(),
-        _dev(free_count, i32, "free_count"), _dev(free_count_out, i32, "free_count_out"), max_rows,
-        _dev(cu_q, i32, "cu_q"), _dev(slots, torch.int64, "slots"), _dev(positions, i32, "positions"),
-        _dev(status, i32, "status"), ws_ptr, ws_bytes, _stream_ptr(stream)), "mx_kv_tables")
+        workspace = workspace if workspace is not None else _new((nbytes,), torch.uint8, block_table, stream)
+        _meta(workspace, "workspace", workspace.dtype)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    else:
+        workspace = None
+    old_, new_, table_, stack_, count_, out_, cu_, slots_, pos_, status_, ws_ = _pointers(
+        old_lens=old_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, free_count=free_count,
+        free_count_out=free_count_out, cu_q=cu_q, slots=slots, positions=positions, status=status, workspace=workspace)
+    _check(lib().mx_kv_tables(old_, new_, B, int(page_size), table_, max_blocks, stack_, free_pages.numel(), count_, out_,
+                              max_rows, cu_, slots_, pos_, status_, ws_, ws_bytes, _stream_ptr(stream)), "mx_kv_tables")
     return cu_q, slots, positions, free_count_out, status
 
 
 def mx_kv_write(k_bf16, v_bf16, slots, cache, page_size: int, stream=None) -> None:
     """Quantize keys and values [T, heads, D] bf16 (rows dense, any row stride) to MXFP4 into the
     cache's slots (int64 [T]; a slot outside the cache writes nothing)."""
-    torch = _torch()
     T, heads, D, k_stride = _rows3(k_bf16, "k_bf16")
-    if tuple(v_bf16.shape) != tuple(k_bf16.shape):
-        raise ValueError(f"v_bf16 must have shape {tuple(k_bf16.shape)}, got {tuple(v_bf16.shape)}")
-    v_stride = _rows3(v_bf16, "v_bf16")[3]
-    _need(slots, "slots", torch.int64, min_numel=T)
+    shape = (T, heads, D)
+    *v_shape, v_stride = _rows3(v_bf16, "v_bf16")
+    if tuple(v_shape) != shape:
+        raise ValueError(f"v_bf16 must have shape {shape}, got {tuple(v_shape)}")
+    _meta(slots, "slots", _torch().int64, T)
     pages = _kv_pages(cache, page_size, heads, D)
     if T == 0:
         return
-    _check(lib().mx_kv_write(_here(k_bf16, "k_bf16"), k_stride, _here(v_bf16, "v_bf16"), v_stride,
-                             _dev(slots, torch.int64, "slots"), T, _dev(cache, torch.uint8, "cache"), pages,
-                             int(page_size), heads, D, _stream_ptr(stream)), "mx_kv_write")
+    k_, v_, slots_, cache_ = _pointers(k_bf16=k_bf16, v_bf16=v_bf16, slots=slots, cache=cache)
+    _check(lib().mx_kv_write(k_, k_stride, v_, v_stride, slots_, T, cache_, pages, int(page_size), heads, D,
+                             _stream_ptr(stream)), "mx_kv_write")
 
 
 def mx_kv_read(cache, slots, heads: int, D: int, page_size: int, k_out=None, v_out=None, stream=None):
     """(k, v) bf16 [T, heads, D]: the values the cache holds at `slots` (int64 [T]); rows whose
     slot is outside the cache are left as they were."""
     torch = _torch()
-    _need(slots, "slots", torch.int64)
-    T = slots.numel()
+    _meta(slots, "slots", torch.int64)
     pages = _kv_pages(cache, page_size, heads, D)
-    k = k_out if k_out is not None else _new((T, heads, D), torch.bfloat16, cache.device, stream)
-    v = v_out if v_out is not None else _new((T, heads, D), torch.bfloat16, cache.device, stream)
-    _need(k, "k_out", torch.bfloat16, shape=(T, heads, D))
-    _need(v, "v_out", torch.bfloat16, shape=(T, heads, D))
-    if T == 0:
+    shape = (slots.numel(), int(heads), int(D))
+    k = k_out if k_out is not None else _new(shape, torch.bfloat16, cache, stream)
+    v = v_out if v_out is not None else _new(shape, torch.bfloat16, cache, stream)
+    for t, name in ((k, "k_out"), (v, "v_out")):
+        _meta(t, name, torch.bfloat16)
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if shape[0] == 0:
         return k, v
-    _check(lib().mx_kv_read(_dev(cache, torch.uint8, "cache"), pages, int(page_size), int(heads), int(D),
-                            _dev(slots, torch.int64, "slots"), T, _dev(k, torch.bfloat16, "k_out"),
-                            _dev(v, torch.bfloat16, "v_out"), _stream_ptr(stream)), "mx_kv_read")
+    cache_, slots_, k_, v_ = _pointers(cache=cache, slots=slots, k_out=k, v_out=v)
+    _check(lib().mx_kv_read(cache_, pages, int(page_size), shape[1], shape[2], slots_, shape[0], k_, v_,
+                            _stream_ptr(stream)), "mx_kv_read")
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
 def mx_kv_attention_workspace_bytes(B: int, T: int, heads_q: int, heads: int, D: int, max_q: int, max_kv: int,
                                     window: int = 0) -> int:
     return int(lib().mx_kv_attention_workspace_bytes(int(B), int(T), int(heads_q), int(heads), int(D), int(max_q),
@@ -584,32 +629,38 @@ def mx_kv_attention(q_bf16, cache, block_table, cu_q, kv_lens, heads: int, page_
     torch = _torch()
     i32 = torch.int32
     T, heads_q, D, q_stride = _rows3(q_bf16, "q_bf16")
-    _need(block_table, "block_table", i32)
+    _meta(block_table, "block_table", i32)
     B, max_blocks = _dims2(block_table, "block_table")
-    _need(cu_q, "cu_q", i32, min_numel=B + 1)
-    _need(kv_lens, "kv_lens", i32, min_numel=B)
+    _meta(cu_q, "cu_q", i32, B + 1)
+    _meta(kv_lens, "kv_lens", i32, B)
+    page_size, heads, window = int(page_size), int(heads), int(window)
     pages = _kv_pages(cache, page_size, heads, D)
-    o = out if out is not None else _new((T, heads_q, D), torch.bfloat16, q_bf16.device, stream)
-    if tuple(o.shape) != (T, heads_q, D):
-        raise ValueError(f"out must have shape {(T, heads_q, D)}, got {tuple(o.shape)}")
-    out_stride = _rows3(o, "out")[3]
+    if out is None:
+        out, out_stride = _new((T, heads_q, D), torch.bfloat16, q_bf16, stream), heads_q * D
+    else:
+        *shape, out_stride = _rows3(out, "out")
+        if tuple(shape) != (T, heads_q, D):
+            raise ValueError(f"out must have shape {(T, heads_q, D)}, got {tuple(shape)}")
     if T == 0 or B == 0:
-        return o
+        return out
     max_q = int(max_q) if max_q is not None else T
-    max_kv = int(max_kv) if max_kv is not None else max_blocks * int(page_size)
+    max_kv = int(max_kv) if max_kv is not None else max_blocks * page_size
     scale = float(scale) if scale is not None else D ** -0.5
     if workspace is None:
         nbytes = mx_kv_attention_workspace_bytes(B, T, heads_q, heads, D, max_q, max_kv, window)
-        workspace = _new((nbytes,), torch.uint8, q_bf16.device, stream) if nbytes else False
-    ws_ptr, ws_bytes = (None, 0)
-    if workspace is not False:
-        ws_ptr, ws_bytes = _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size()
-    _check(lib().mx_kv_attention(
-        _here(q_bf16, "q_bf16"), q_stride, _dev(cache, torch.uint8, "cache"), pages, int(page_size),
-        _dev(block_table, i32, "block_table"), max_blocks, _dev(cu_q, i32, "cu_q"), _dev(kv_lens, i32, "kv_lens"), B, T,
-        heads_q, int(heads), D, max_q, max_kv, int(bool(causal)), int(window), scale, _here(o, "out"), out_stride,
-        ws_ptr, ws_bytes, _stream_ptr(stream)), "mx_kv_attention")
-    return o
+        workspace = _new((nbytes,), torch.uint8, q_bf16, stream) if nbytes else None
+    elif workspace is False:
+        workspace = None
+    ws_bytes = 0
+    if workspace is not None:
+        _meta(workspace, "workspace", workspace.dtype)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    q_, cache_, table_, cu_, kv_, out_, ws_ = _pointers(q_bf16=q_bf16, cache=cache, block_table=block_table, cu_q=cu_q,
+                                                        kv_lens=kv_lens, out=out, workspace=workspace)
+    _check(lib().mx_kv_attention(q_, q_stride, cache_, pages, page_size, table_, max_blocks, cu_, kv_, B, T, heads_q, heads,
+                                 D, max_q, max_kv, 1 if causal else 0, window, scale, out_, out_stride, ws_, ws_bytes,
+                                 _stream_ptr(stream)), "mx_kv_attention")
+    return out
 
 
 def mx_kv_attention_plan(B: int, T: int, heads_q: int, heads: int, D: int, max_q: int, max_kv: int, window: int = 0,

@@ -161,8 +161,8 @@ __device__ __forceinline__ float scale_at(uint32_t w, uint32_t shift) {
 
 // ------------------------------------------------------------------------------- few rows
 //
-// Decoding and drafts: one workgroup of four waves takes a tile of 16 NT rows and C tokens of one
-// head, each wave a quarter of them on its own, 32 tokens a step; the next step's keys are fetched
+// Decoding and drafts: a workgroup takes a tile of 16 NT rows and a run of tokens of one head,
+// each wave its part of them on its own, 32 tokens a step; the next step's keys are fetched
 // when this step's are in the products, its values likewise. The transposed products put a query row in each of the 16 columns:
 //   S^T (16 tokens x 16 rows) = K Q^T    scaled 16x16x128 MFMA, A = K codes from the cache,
 //   O^T (D x 16 rows)        += V^T P^T  bf16 16x16x32 MFMA, A = V decoded in registers.
@@ -176,7 +176,7 @@ template <int D>
 struct TokenTile {  // one lane's share of 16 tokens
   static constexpr int M = D / 32;
   u32x4 k[(D + 127) / 128];
-  uint32_t ks[(D + 127) / 128];
+  uint32_t ks[(D + 127) / 128];  // the word that holds the token's scale byte, at bit 8 (token % 4)
   uint32_t v[M];   // word j: the lane's element pair of scale block j, four tokens
   uint32_t vs[M];  // the 4 M scale bytes of its four tokens
 
@@ -185,12 +185,12 @@ struct TokenTile {  // one lane's share of 16 tokens
     const uint8_t* kb = blk + P * D + in_page * (D / 2);
     if constexpr (D == 64) {
       k[0] = *reinterpret_cast<const u32x4*>(kc + (lane & 31u) * 16u);
-      ks[0] = kb[lane & 31u];
+      ks[0] = *reinterpret_cast<const uint32_t*>(kb + (lane & 28u));
     } else {
 #pragma unroll
       for (int c = 0; c < D / 128; ++c) {
         k[c] = *reinterpret_cast<const u32x4*>(kc + (c * 1024u + lane * 16u));
-        ks[c] = kb[c * 64u + lane];
+        ks[c] = *reinterpret_cast<const uint32_t*>(kb + (c * 64u + (lane & 60u)));
       }
     }
   }
@@ -225,143 +225,174 @@ struct TokenTile {  // one lane's share of 16 tokens
   }
 };
 
-constexpr int kFewWaves = 4;
+// Waves a SIMD that the registers allow without spilling.
+constexpr int few_occupancy(int D, int NT) { return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 3 : 2) : 2; }
+
 constexpr int kAllRows = 0x7FFFFFFF;
 
-// How a kernel cuts: rows of a tile, tokens of a split, most splits.
-struct KvSplit {
-  int R, C, S;
+// Work is cut into equal shares, however ragged the lengths are: a segment is a row tile and a
+// head, of ceil(tokens / 32) + kSegmentUnits units (a segment's start costs about as much as that
+// many units of 32 tokens); the segments of all requests lie in a row, and worker i of 2^lg takes
+// the units floor(i W / 2^lg) on of all W. A segment that lies in one share is written to the
+// output; of one that is cut, each worker leaves an unscaled part: in its slot 0 if the segment is
+// its first, else in its slot 1 (its last). The worker whose share begins in the second part of a
+// segment names the parts to the join.
+// Without a workspace a worker takes the whole segments that begin in its share.
+constexpr int kSegmentUnits = 4;
+
+struct KvShares {
+  int lg;         // log2 of the workers
+  int rows_most;  // requests of more rows (query rows times group) are the other kernel's
+  float* o;       // [workers][2][R][D], or null: no segment is cut
+  float2* ml;     // [workers][2][R]: maximum, sum
+  int4* seams;    // [workers]: first query row; first row of the tile; head | rows << 16; parts | slot of the first << 30
 };
-// Partial results of split rows in the workspace: unscaled sums o [S][T][Hq][D] with their maximum
-// and sum of weights ml [S][T][Hq], and in how many splits a row is, count [T][Hq] (1: the row is
-// in the output already). All null where nothing is split.
-struct KvParts {
-  float* o;
-  float2* ml;
-  int32_t* count;
-  __device__ __forceinline__ int64_t at(const KvAttnArgs& a, int split, int t, int hq) const {
-    return ((int64_t)split * a.T + t) * a.Hq + hq;
+
+struct KvRequest {
+  int q0, n, len;
+  __device__ __forceinline__ int tiles(int G, int R) const { return (n * G + R - 1) / R; }
+  __device__ __forceinline__ int units(const KvAttnArgs& a) const {  // of each of its segments
+    const int lo = row_begin(a, len - n) & ~15, hi = row_end(a, len, len - 1);
+    return max(hi - lo + 31, 0) / 32 + kSegmentUnits;
   }
 };
 
-// Waves a SIMD that the registers allow without spilling.
-constexpr int few_occupancy(int D, int NT) { return D == 64 ? (NT == 1 ? 5 : 3) : D == 128 ? (NT == 1 ? 4 : 2) : 2; }
+__device__ __forceinline__ KvRequest request_of(const KvAttnArgs& a, int b, int rows_most) {
+  KvRequest r = {0, 0, 0};
+  if (b < a.B) {
+    r.q0 = clamp_int(a.cu_q[b], 0, a.T);
+    r.n = clamp_int(a.cu_q[b + 1], r.q0, a.T) - r.q0;
+    r.len = (int)min((int64_t)max(a.kv_lens[b], 0), (int64_t)a.max_blocks << a.log2_page);
+    if (r.n * (int64_t)a.G > rows_most) r.n = 0;
+  }
+  return r;
+}
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
 template <int D, int NT>
-__global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_attn_few(KvAttnArgs a, int rows_most,
-                                                                                      KvSplit k, KvParts out) {
+__global__ __launch_bounds__(kThreads, few_occupancy(D, NT)) void k_kv_attn_few(KvAttnArgs a, KvShares sh) {
   constexpr int R = 16 * NT, M = D / 32, KC = (D + 127) / 128, LD = D + 4;
-  __shared__ float o_all[kFewWaves][16][LD];
-  __shared__ float2 ml_all[kFewWaves][R];
+  __shared__ float o_all[kWaves][16][LD];
+  __shared__ float2 ml_all[kWaves][R];
+  __shared__ int64_t sums[kThreads + 1];  // units before each thread's requests
+  __shared__ KvRequest requests[kThreads];
+  __shared__ int64_t wave_sum[kWaves];
+  __shared__ int found;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
-  const int C = k.C, S = k.S, split = (int)(blockIdx.x % S), h = (int)(blockIdx.x / S % a.H), tile = (int)(blockIdx.x / S / a.H);
-  RowTile w;
-  if (rows_most == kAllRows) {
-    if (!find_row_tile(a, R, tile, w)) return;
-  } else if (!row_tile_of(a, R, tile, 0, w) || w.n * a.G > rows_most) {  // a tile a request; larger ones are
-    return;                                                              // the other kernel's
-  }
-  const int splits = splits_of(w, C, S);
-  if (split >= splits) return;
 
-  // the queries, split in two
-  v8i q_hi[NT][KC], q_lo[NT][KC];
-  uint32_t q_sc[NT];
-  int row_lo[NT], row_hi[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = w.rb + min(16 * nt + col, w.rows - 1);  // columns past the last row repeat it
-    const uint16_t* src = a.q + (int64_t)(w.q0 + r / a.G) * a.q_stride + (h * a.G + r % a.G) * D;
-    uint4 x[2 * KC];
-    uint32_t E = 0;
-    if constexpr (D == 64) {  // each lane group 16 elements
-      x[0] = reinterpret_cast<const uint4*>(src)[2 * g];
-      x[1] = reinterpret_cast<const uint4*>(src)[2 * g + 1];
-      E = top_exponent(x[1], top_exponent(x[0], 0));
-      E = max(E, (uint32_t)__shfl_xor((int)E, 16));
-      E = max(E, (uint32_t)__shfl_xor((int)E, 32));
-    } else {
-      uint4 y[4 * KC];
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)  // bytes 0..15: elements 16 g, bytes 16..31: 64 + 16 g
-          y[4 * c + i] = reinterpret_cast<const uint4*>(src + 128 * c + 64 * (i / 2) + 16 * g)[i % 2];
-#pragma unroll
-      for (int i = 0; i < 4 * KC; ++i) E = top_exponent(y[i], E);
-      E = max(E, (uint32_t)__shfl_xor((int)E, 16));
-      E = max(E, (uint32_t)__shfl_xor((int)E, 32));
-      const float down = __builtin_bit_cast(float, (254u - query_scale(E)) << 23);
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 u = y[4 * c + 2 * i], v = y[4 * c + 2 * i + 1];
-          const uint32_t e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-          uint32_t hi[4], lo[4];
-          split_fp8(e, down, hi, lo);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            q_hi[nt][c][4 * i + j] = (int)hi[j];
-            q_lo[nt][c][4 * i + j] = (int)lo[j];
-          }
-        }
-    }
-    const uint32_t sc = query_scale(E);
-    if constexpr (D == 64) {
-      // one 16x16x128 product takes both parts: k < 64 is hi (bytes 0..15), k >= 64 lo, over the
-      // same keys given twice (lane groups 2 and 3 load what 0 and 1 do)
-      const float down = __builtin_bit_cast(float, (254u - sc) << 23);
-      const uint32_t e[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-      uint32_t hi[4], lo[4];
-      split_fp8(e, down, hi, lo);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q_hi[nt][0][j] = (int)hi[j];
-        q_hi[nt][0][4 + j] = (int)lo[j];
-      }
-      q_sc[nt] = g < 2 ? sc : sc - 5u;
-    } else {
-      q_sc[nt] = sc;
-    }
-    const int pos = w.pos(r, a.G);
-    row_lo[nt] = row_begin(a, pos);
-    row_hi[nt] = row_end(a, w.len, pos);
+  // where the shares lie: a sum over the requests, each thread `per` of them
+  const int per = (a.B + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const KvRequest r = request_of(a, threadIdx.x * per + i, sh.rows_most);
+    if (i == 0) requests[threadIdx.x] = r;
+    if (r.n > 0) mine += (int64_t)r.tiles(a.G, R) * a.H * r.units(a);
   }
+  int64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t y = __shfl_up(upto, d);
+    if (lane >= d) upto += y;
+  }
+  if (lane == 63) wave_sum[wave] = upto;
+  __syncthreads();
+  int64_t W = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    if (i == wave) upto += W;
+    W += wave_sum[i];
+  }
+  int lg = sh.lg;
+  while (lg > 0 && (W >> lg) == 0) --lg;  // a unit a worker at least
+  const int worker = (int)blockIdx.x;
+  if (W == 0 || worker >> lg) {
+    if (threadIdx.x == 0 && sh.o) sh.seams[worker].w = 0;
+    return;
+  }
+  auto share_at = [&](int i) { return i * (W >> lg) + ((i * (W & (((int64_t)1 << lg) - 1))) >> lg); };  // i W / 2^lg
+  int64_t u = share_at(worker);
+  const int64_t u_end = share_at(worker + 1);
+  sums[threadIdx.x] = upto - mine;
+  if (threadIdx.x == kThreads - 1) sums[kThreads] = W;
+  if (upto - mine <= u && u < upto) found = threadIdx.x;
+  __syncthreads();
+  int b = __builtin_amdgcn_readfirstlane(found) * per;
+  int64_t before = sums[__builtin_amdgcn_readfirstlane(found)];  // units before request b
 
-  // this wave's tokens
-  const int t0 = w.lo + split * C;
-  const int t1 = split == S - 1 ? w.hi : min(w.hi, t0 + C);
-  const int share = ((t1 - t0 + 32 * kFewWaves - 1) / (32 * kFewWaves)) * 32;
-  const int w0 = t0 + wave * share, w1 = min(t1, w0 + share);
-  // a step inside [all_lo, all_hi) needs no mask
-  const int all_lo = row_begin(a, w.pos(w.rb + w.rows - 1, a.G)), all_hi = min(w1, row_end(a, w.len, w.pos(w.rb, a.G)));
   const float c2 = a.scale * kLog2e;
   uint32_t shift = 23;
   asm volatile("" : "+v"(shift));  // kept in a register: scale_at
   const int P = 1 << a.log2_page;
-  const int32_t* table = a.block_table + (int64_t)w.b * a.max_blocks;
 
-  float m[NT], l[NT];
-  v4f o[NT][2 * M];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = kLowest;
-    l[nt] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 2 * M; ++j) o[nt][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-  }
-
-  for (int base = w0; base < w1; base += 64 * 16) {  // 64 token tiles whose pages one load fetches
-    const int tiles = min(64, (w1 - base + 15) >> 4);
-    int page = 0;
-    bool bad = false;
-    if (lane < tiles) {
-      page = table[(base + 16 * lane) >> a.log2_page];
-      bad = page < 0 || page >= a.num_pages;
-      if (bad) page = 0;
+  for (bool first = true; u < u_end; first = false) {
+    // the segment of unit u
+    KvRequest req;
+    int units;
+    int64_t all;
+    for (;; ++b) {  // u < W: some request ends after it
+      req = per == 1 ? requests[b] : request_of(a, b, sh.rows_most);
+      units = __builtin_amdgcn_readfirstlane(req.units(a));
+      all = req.n > 0 ? (int64_t)req.tiles(a.G, R) * a.H * units : 0;
+      if (u < before + all) break;
+      before += all;
     }
-    const uint64_t bad_tiles = __ballot(bad);
+    const int64_t in = u - before;
+    const int seg = (in >> 31) ? (int)(in / units) : (int)((uint32_t)in / (uint32_t)units);  // head fastest
+    const int from = (int)(in - (int64_t)seg * units), h = seg % a.H;
+    const int64_t seg_start = u - from, seg_end = seg_start + units;
+    RowTile w;
+    w.b = b;
+    w.q0 = __builtin_amdgcn_readfirstlane(req.q0);
+    w.n = __builtin_amdgcn_readfirstlane(req.n);
+    w.len = __builtin_amdgcn_readfirstlane(req.len);
+    w.rb = seg / a.H * R;
+    w.rows = min(R, w.n * a.G - w.rb);
+    w.lo = row_begin(a, w.pos(w.rb, a.G)) & ~15;
+    w.hi = row_end(a, w.len, w.pos(w.rb + w.rows - 1, a.G));
+    int t0 = w.lo, t1 = w.hi;
+    bool whole = true;
+    if (sh.o) {
+      const int to = (int)(min(u_end, seg_end) - seg_start);
+      whole = from == 0 && to == units;
+      t0 = w.lo + 32 * max(from - kSegmentUnits, 0);
+      if (to < units) t1 = min(t1, w.lo + 32 * max(to - kSegmentUnits, 0));
+      if (first && threadIdx.x == 0) {
+        const int64_t u_before = share_at(worker - 1);
+        int4 seam = make_int4(w.q0, w.rb, h | (w.rows << 16), 0);
+        if (from > 0 && seg_start >= u_before) {  // the share before this one holds the segment's first part
+          int last = worker, past = 1 << lg;  // the last share that begins in the segment
+          while (past - last > 1) {
+            const int mid = (last + past) >> 1;
+            if (share_at(mid) < seg_end) last = mid; else past = mid;
+          }
+          seam.w = (last - worker + 2) | (seg_start > u_before ? 1 << 30 : 0);
+        }
+        sh.seams[worker] = seam;
+      }
+    } else if (from > 0) {  // begun in an earlier share
+      u = seg_end;
+      continue;
+    }
+    u = seg_end;
+
+    // this wave's tokens
+    const int share = (max(t1 - t0, 0) + 32 * kWaves - 1) / (32 * kWaves) * 32;
+    const int w0 = t0 + wave * share, w1 = min(t1, w0 + share);
+    const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
+    int base = w0, tiles = 0, page = 0;
+    uint64_t bad_tiles = 0;
+    auto fetch_pages = [&]() {  // of 64 token tiles from base on, one a lane
+      tiles = min(64, (w1 - base + 15) >> 4);
+      page = 0;
+      bool bad = false;
+      if (lane < tiles) {
+        page = table[(base + 16 * lane) >> a.log2_page];
+        bad = page < 0 || page >= a.num_pages;
+        if (bad) page = 0;
+      }
+      bad_tiles = __ballot(bad);
+    };
     auto block_of = [&](int tile, int& in_page) {
       in_page = ((base + 16 * tile) & (P - 1)) >> 4;
       return a.cache + ((int64_t)__builtin_amdgcn_readlane(page, tile) * a.H + h) * a.block_bytes;
@@ -371,7 +402,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_att
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         int in_page;
-        const uint8_t* blk = block_of(min(2 * step + i, tiles - 1), in_page);
+        const uint8_t* blk = block_of(max(min(2 * step + i, tiles - 1), 0), in_page);
         x[i].load_k(blk, P, in_page, lane);
       }
     };
@@ -379,155 +410,324 @@ __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_att
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         int in_page;
-        const uint8_t* blk = block_of(min(2 * step + i, tiles - 1), in_page);
+        const uint8_t* blk = block_of(max(min(2 * step + i, tiles - 1), 0), in_page);
         x[i].load_v(blk, P, in_page, lane);
       }
     };
-    const int steps = (tiles + 1) >> 1;
+    // The chain of loads is lengths, pages, tokens; the queries come meanwhile. A wave without
+    // tokens fetches some of page 0, unused: without a branch the waits can tell the loads apart.
+    fetch_pages();
+    uint4 y[NT][D == 64 ? 2 : 4 * KC];
+    int row_lo[NT], row_hi[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = w.rb + min(16 * nt + col, w.rows - 1);  // columns past the last row repeat it
+      const uint16_t* src = a.q + (int64_t)(w.q0 + r / a.G) * a.q_stride + (h * a.G + r % a.G) * D;
+      if constexpr (D == 64) {  // each lane group 16 elements
+        y[nt][0] = reinterpret_cast<const uint4*>(src)[2 * g];
+        y[nt][1] = reinterpret_cast<const uint4*>(src)[2 * g + 1];
+      } else {
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // bytes 0..15: elements 16 g, bytes 16..31: 64 + 16 g
+            y[nt][4 * c + i] = reinterpret_cast<const uint4*>(src + 128 * c + 64 * (i / 2) + 16 * g)[i % 2];
+      }
+      const int pos = w.pos(r, a.G);
+      row_lo[nt] = row_begin(a, pos);
+      row_hi[nt] = row_end(a, w.len, pos);
+    }
     load_k(0);
     load_v(0);
-    for (int step = 0; step < steps; ++step) {
-      const int t = base + 32 * step;
-      v4f s[NT][2];
+
+    // the queries, split in two
+    v8i q_hi[NT][KC], q_lo[NT][KC];
+    uint32_t q_sc[NT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t E = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          s[nt][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < (D == 64 ? 2 : 4 * KC); ++i) E = top_exponent(y[nt][i], E);
+      E = max(E, (uint32_t)__shfl_xor((int)E, 16));
+      E = max(E, (uint32_t)__shfl_xor((int)E, 32));
+      const uint32_t sc = query_scale(E);
+      const float down = __builtin_bit_cast(float, (254u - sc) << 23);
+      if constexpr (D == 64) {
+        // one 16x16x128 product takes both parts: k < 64 is hi (bytes 0..15), k >= 64 lo, over the
+        // same keys given twice (lane groups 2 and 3 load what 0 and 1 do)
+        const uint32_t e[8] = {y[nt][0].x, y[nt][0].y, y[nt][0].z, y[nt][0].w, y[nt][1].x, y[nt][1].y, y[nt][1].z, y[nt][1].w};
+        uint32_t hi[4], lo[4];
+        split_fp8(e, down, hi, lo);
 #pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const v8i kv = {(int)x[i].k[c].x, (int)x[i].k[c].y, (int)x[i].k[c].z, (int)x[i].k[c].w, 0, 0, 0, 0};
-            s[nt][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kv, q_hi[nt][c], s[nt][i], 4, 0, 0,
-                                                                        (int)x[i].ks[c], 0, (int)q_sc[nt]);
-            if constexpr (D != 64)
-              s[nt][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kv, q_lo[nt][c], s[nt][i], 4, 0, 0,
-                                                                          (int)x[i].ks[c], 0, (int)(q_sc[nt] - 5u));
+        for (int j = 0; j < 4; ++j) {
+          q_hi[nt][0][j] = (int)hi[j];
+          q_hi[nt][0][4 + j] = (int)lo[j];
+        }
+        q_sc[nt] = g < 2 ? sc : sc - 5u;
+      } else {
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 p0 = y[nt][4 * c + 2 * i], p1 = y[nt][4 * c + 2 * i + 1];
+            const uint32_t e[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+            uint32_t hi[4], lo[4];
+            split_fp8(e, down, hi, lo);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              q_hi[nt][c][4 * i + j] = (int)hi[j];
+              q_lo[nt][c][4 * i + j] = (int)lo[j];
+            }
+          }
+        q_sc[nt] = sc;
+      }
+    }
+    // a step inside [all_lo, all_hi) needs no mask
+    const int all_lo = row_begin(a, w.pos(w.rb + w.rows - 1, a.G)), all_hi = min(w1, row_end(a, w.len, w.pos(w.rb, a.G)));
+
+    float m[NT], l[NT];
+    v4f o[NT][2 * M];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = kLowest;
+      l[nt] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2 * M; ++j) o[nt][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+    }
+
+    while (base < w1) {
+      const int steps = (tiles + 1) >> 1;
+      for (int step = 0; step < steps; ++step) {
+        const int t = base + 32 * step;
+        v4f s[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            s[nt][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+              const int ks = (int)(x[i].ks[c] >> (8 * (lane & 3)));  // the product takes its low byte
+              const v8i kv = {(int)x[i].k[c].x, (int)x[i].k[c].y, (int)x[i].k[c].z, (int)x[i].k[c].w, 0, 0, 0, 0};
+              s[nt][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kv, q_hi[nt][c], s[nt][i], 4, 0, 0, ks, 0,
+                                                                          (int)q_sc[nt]);
+              if constexpr (D != 64)
+                s[nt][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kv, q_lo[nt][c], s[nt][i], 4, 0, 0, ks, 0,
+                                                                            (int)(q_sc[nt] - 5u));
+            }
+          }
+        load_k(min(step + 1, steps - 1));  // the last step's loads, of what it has already, go unused
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][i][e] *= c2;
+        const uint64_t bad2 = bad_tiles >> (2 * step);
+        if (t < all_lo || t + 32 > all_hi || (bad2 & 3u)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int tt = t + 16 * i + 4 * g;
+            const bool hidden = (bad2 >> i) & 1u;
+            x[i].mask(tt, w.lo, hidden ? 0 : w1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (hidden || tt + e < row_lo[nt] || tt + e >= min(row_hi[nt], w1)) s[nt][i][e] = -INFINITY;
           }
         }
-      load_k(min(step + 1, steps - 1));  // the last step's loads, of what it has already, go unused
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][i][e] *= c2;
-      const uint64_t bad2 = bad_tiles >> (2 * step);
-      if (t < all_lo || t + 32 > all_hi || (bad2 & 3u)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int tt = t + 16 * i + 4 * g;
-          const bool hidden = (bad2 >> i) & 1u;
-          x[i].mask(tt, w.lo, hidden ? 0 : w1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (hidden || tt + e < row_lo[nt] || tt + e >= min(row_hi[nt], w1)) s[nt][i][e] = -INFINITY;
-        }
-      }
-      uint32_t p[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float top = fmaxf(fmaxf(fmaxf(s[nt][0][0], s[nt][0][1]), fmaxf(s[nt][0][2], s[nt][0][3])),
-                          fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
-        // The maximum in use may lag behind the true one by kLag (weights up to 2^kLag, all sums
-        // in FP32); only past that are the sums rescaled.
-        if (__any(top > m[nt] + kLag)) {
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float m1 = fmaxf(m[nt], top), alpha = __builtin_amdgcn_exp2f(m[nt] - m1);
-          m[nt] = m1;
-          l[nt] *= alpha;
-#pragma unroll
-          for (int j = 0; j < 2 * M; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][j][e] *= alpha;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; e += 2)
-            p[nt][2 * i + e / 2] = pack_bf16(__builtin_amdgcn_exp2f(s[nt][i][e] - m[nt]),
-                                             __builtin_amdgcn_exp2f(s[nt][i][e + 1] - m[nt]));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l[nt] = add_pair(l[nt], p[nt][i]);
-      }
-      static_for<M>([&](auto J) {
-        constexpr int j = J;
-        uint32_t even[4], odd[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t c0 = decode2<0>(x[i].v[j], x[i].template scale<0, j>(shift));
-          const uint32_t c1 = decode2<1>(x[i].v[j], x[i].template scale<1, j>(shift));
-          const uint32_t c2_ = decode2<2>(x[i].v[j], x[i].template scale<2, j>(shift));
-          const uint32_t c3 = decode2<3>(x[i].v[j], x[i].template scale<3, j>(shift));
-          even[2 * i] = __builtin_amdgcn_perm(c1, c0, 0x05040100);
-          even[2 * i + 1] = __builtin_amdgcn_perm(c3, c2_, 0x05040100);
-          odd[2 * i] = __builtin_amdgcn_perm(c1, c0, 0x07060302);
-          odd[2 * i + 1] = __builtin_amdgcn_perm(c3, c2_, 0x07060302);
-        }
-        const bf16x8 ve = as_bf16x8(even[0], even[1], even[2], even[3]), vo = as_bf16x8(odd[0], odd[1], odd[2], odd[3]);
+        uint32_t p[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const bf16x8 pt = as_bf16x8(p[nt][0], p[nt][1], p[nt][2], p[nt][3]);
-          o[nt][2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ve, pt, o[nt][2 * j], 0, 0, 0);
-          o[nt][2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vo, pt, o[nt][2 * j + 1], 0, 0, 0);
+          float top = fmaxf(fmaxf(fmaxf(s[nt][0][0], s[nt][0][1]), fmaxf(s[nt][0][2], s[nt][0][3])),
+                            fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
+          // The maximum in use may lag behind the true one by kLag (weights up to 2^kLag, all sums
+          // in FP32); only past that are the sums rescaled.
+          if (__any(top > m[nt] + kLag)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m1 = fmaxf(m[nt], top), alpha = __builtin_amdgcn_exp2f(m[nt] - m1);
+            m[nt] = m1;
+            l[nt] *= alpha;
+#pragma unroll
+            for (int j = 0; j < 2 * M; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][j][e] *= alpha;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+              p[nt][2 * i + e / 2] = pack_bf16(__builtin_amdgcn_exp2f(s[nt][i][e] - m[nt]),
+                                               __builtin_amdgcn_exp2f(s[nt][i][e + 1] - m[nt]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[nt] = add_pair(l[nt], p[nt][i]);
         }
-      });
-      load_v(min(step + 1, steps - 1));
+        static_for<M>([&](auto J) {
+          constexpr int j = J;
+          uint32_t even[4], odd[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t c0 = decode2<0>(x[i].v[j], x[i].template scale<0, j>(shift));
+            const uint32_t c1 = decode2<1>(x[i].v[j], x[i].template scale<1, j>(shift));
+            const uint32_t c2_ = decode2<2>(x[i].v[j], x[i].template scale<2, j>(shift));
+            const uint32_t c3 = decode2<3>(x[i].v[j], x[i].template scale<3, j>(shift));
+            even[2 * i] = __builtin_amdgcn_perm(c1, c0, 0x05040100);
+            even[2 * i + 1] = __builtin_amdgcn_perm(c3, c2_, 0x05040100);
+            odd[2 * i] = __builtin_amdgcn_perm(c1, c0, 0x07060302);
+            odd[2 * i + 1] = __builtin_amdgcn_perm(c3, c2_, 0x07060302);
+          }
+          const bf16x8 ve = as_bf16x8(even[0], even[1], even[2], even[3]), vo = as_bf16x8(odd[0], odd[1], odd[2], odd[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const bf16x8 pt = as_bf16x8(p[nt][0], p[nt][1], p[nt][2], p[nt][3]);
+            o[nt][2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ve, pt, o[nt][2 * j], 0, 0, 0);
+            o[nt][2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vo, pt, o[nt][2 * j + 1], 0, 0, 0);
+          }
+        });
+        load_v(min(step + 1, steps - 1));
+      }
+      base += 64 * 16;
+      if (base >= w1) break;
+      fetch_pages();
+      load_k(0);
+      load_v(0);
     }
-  }
 
-  // join the waves: the largest maximum, every wave's sums at it, added in the waves' order
+    // join the waves: the largest maximum, every wave's sums at it, added in the waves' order
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    l[nt] += __shfl_xor(l[nt], 16);
-    l[nt] += __shfl_xor(l[nt], 32);
-    if (g == 0) ml_all[wave][16 * nt + col] = make_float2(m[nt], l[nt]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float top = kLowest;
-#pragma unroll
-    for (int i = 0; i < kFewWaves; ++i) top = fmaxf(top, ml_all[i][16 * nt + col].x);
-    const float f = __builtin_amdgcn_exp2f(m[nt] - top);
-    if (nt > 0) __syncthreads();
-#pragma unroll
-    for (int j = 0; j < M; ++j) {
-      const v4f e = o[nt][2 * j], d = o[nt][2 * j + 1];
-      *reinterpret_cast<v4f*>(&o_all[wave][col][32 * j + 8 * g]) = (v4f){e[0] * f, d[0] * f, e[1] * f, d[1] * f};
-      *reinterpret_cast<v4f*>(&o_all[wave][col][32 * j + 8 * g + 4]) = (v4f){e[2] * f, d[2] * f, e[3] * f, d[3] * f};
+    for (int nt = 0; nt < NT; ++nt) {
+      l[nt] += __shfl_xor(l[nt], 16);
+      l[nt] += __shfl_xor(l[nt], 32);
+      if (g == 0) ml_all[wave][16 * nt + col] = make_float2(m[nt], l[nt]);
     }
     __syncthreads();
-    constexpr int E = D / 16;  // elements of a thread
-    const int cr = threadIdx.x / 16, d0 = (threadIdx.x % 16) * E;
-    if (16 * nt + cr >= w.rows) continue;
-    float M1 = kLowest, L = 0.f, x[E];
+    const int64_t slot = (int64_t)worker * 2 + (first ? 0 : 1);
 #pragma unroll
-    for (int i = 0; i < kFewWaves; ++i) M1 = fmaxf(M1, ml_all[i][16 * nt + cr].x);
+    for (int nt = 0; nt < NT; ++nt) {
+      float top = kLowest;
 #pragma unroll
-    for (int i = 0; i < kFewWaves; ++i) L += ml_all[i][16 * nt + cr].y * __builtin_amdgcn_exp2f(ml_all[i][16 * nt + cr].x - M1);
+      for (int i = 0; i < kWaves; ++i) top = fmaxf(top, ml_all[i][16 * nt + col].x);
+      const float f = __builtin_amdgcn_exp2f(m[nt] - top);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      x[e] = o_all[0][cr][d0 + e];
+      for (int j = 0; j < M; ++j) {
+        const v4f e = o[nt][2 * j], d = o[nt][2 * j + 1];
+        *reinterpret_cast<v4f*>(&o_all[wave][col][32 * j + 8 * g]) = (v4f){e[0] * f, d[0] * f, e[1] * f, d[1] * f};
+        *reinterpret_cast<v4f*>(&o_all[wave][col][32 * j + 8 * g + 4]) = (v4f){e[2] * f, d[2] * f, e[3] * f, d[3] * f};
+      }
+      __syncthreads();
+      constexpr int E = D / 16;  // a thread's elements
+      const int cr = 16 * nt + threadIdx.x / 16, d0 = (threadIdx.x % 16) * E;
+      if (cr < w.rows) {
+        float M1 = kLowest, L = 0.f, z[E];
 #pragma unroll
-      for (int i = 1; i < kFewWaves; ++i) x[e] += o_all[i][cr][d0 + e];
+        for (int i = 0; i < kWaves; ++i) M1 = fmaxf(M1, ml_all[i][cr].x);
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) L += ml_all[i][cr].y * __builtin_amdgcn_exp2f(ml_all[i][cr].x - M1);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          z[e] = o_all[0][cr - 16 * nt][d0 + e];
+#pragma unroll
+          for (int i = 1; i < kWaves; ++i) z[e] += o_all[i][cr - 16 * nt][d0 + e];
+        }
+        if (whole) {
+          const int r = w.rb + cr;
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          uint16_t* dst = a.out + (int64_t)(w.q0 + r / a.G) * a.out_stride + (h * a.G + r % a.G) * D + d0;
+#pragma unroll
+          for (int e = 0; e < E; e += 4)
+            *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16(z[e] * inv, z[e + 1] * inv), pack_bf16(z[e + 2] * inv, z[e + 3] * inv));
+        } else {
+          float* dst = sh.o + (slot * R + cr) * D + d0;
+#pragma unroll
+          for (int e = 0; e < E; e += 4) *reinterpret_cast<v4f*>(dst + e) = (v4f){z[e], z[e + 1], z[e + 2], z[e + 3]};
+          if (threadIdx.x % 16 == 0) sh.ml[slot * R + cr] = make_float2(M1, L);
+        }
+      }
+      __syncthreads();  // before the next rows', or the next segment's, sums take the place
     }
-    const int r = w.rb + 16 * nt + cr, t = w.q0 + r / a.G, hq = h * a.G + r % a.G;
-    if (splits == 1) {
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      uint16_t* dst = a.out + (int64_t)t * a.out_stride + hq * D + d0;
+  }
+}
+
+// Joins the parts of the segments that shares have cut: a workgroup for `each` workers and four rows
+// (more in turn), W waves a row, each every W-th part. The segment's first part is in the worker before,
+// in the slot that the seam names; the others in the slots 0 from the worker on. The parts' weights
+// are worked out 64 at a time, one a lane, so that the loads of the sums wait for nothing.
+template <int D, int W>
+__global__ __launch_bounds__(256 * W) void k_kv_attn_seams(KvAttnArgs a, KvShares sh, int R, int each) {
+  constexpr int E = D / 64;
+  typedef float vec __attribute__((ext_vector_type(E)));
+  __shared__ vec o_all[4 * W][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wave % W;
+  const int first = (int)blockIdx.x * each;
+  for (int worker = first; worker < min(first + each, 1 << sh.lg); ++worker) {
+    const int4 seam = sh.seams[worker];
+    const int parts = seam.w & 0x3FFFFFFF, rows = parts ? seam.z >> 16 : 0, h = seam.z & 0xFFFF;
+    for (int r0 = 4 * (int)blockIdx.y; r0 < rows; r0 += 4 * (int)gridDim.y) {
+      const int r = r0 + wave / W;
+      float l = 0.f;
+      vec x;
 #pragma unroll
-      for (int e = 0; e < E; e += 4)
-        *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16(x[e] * inv, x[e + 1] * inv), pack_bf16(x[e + 2] * inv, x[e + 3] * inv));
-    } else {
-      float* dst = out.o + out.at(a, split, t, hq) * D + d0;
+      for (int e = 0; e < E; ++e) x[e] = 0.f;
+      if (r < rows) {
+        // part i's row: in the slots 2 (worker - 1 + i), the first part's one later if the seam says so
+        auto at = [&](int i) { return ((int64_t)2 * (worker - 1 + i) + (i == 0 ? (seam.w >> 30) & 1 : 0)) * R + r; };
+        float m = kLowest;
+        for (int i = lane; i < parts; i += 64) m = fmaxf(m, sh.ml[at(i)].x);
 #pragma unroll
-      for (int e = 0; e < E; e += 4) *reinterpret_cast<v4f*>(dst + e) = (v4f){x[e], x[e + 1], x[e + 2], x[e + 3]};
-      if (threadIdx.x % 16 == 0) out.ml[out.at(a, split, t, hq)] = make_float2(M1, L);
+        for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        for (int i0 = 0; i0 < parts; i0 += 64) {
+          float f = 0.f;
+          if (i0 + lane < parts) {
+            const float2 ml = sh.ml[at(i0 + lane)];
+            f = __builtin_amdgcn_exp2f(ml.x - m);
+            l += ml.y * f;
+          }
+          const int n = min(64, parts - i0);
+          for (int i = sub; i < n; i += 4 * W) {  // four parts' loads at once; past the last, that one with weight 0
+            vec y[4];
+            float g[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int j = min(i + W * k, n - 1);
+              y[k] = *reinterpret_cast<const vec*>(sh.o + at(i0 + j) * D + lane * E);
+              g[k] = i + W * k < n ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), j)) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int e = 0; e < E; ++e) x[e] += y[k][e] * g[k];
+          }
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+      }
+      if constexpr (W > 1) {
+        o_all[wave][lane] = x;
+        __syncthreads();
+      }
+      if (r < rows && sub == 0) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int row = seam.y + r;
+        uint16_t* dst = a.out + (int64_t)(seam.x + row / a.G) * a.out_stride + (h * a.G + row % a.G) * D + lane * E;
+        float z[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          z[e] = x[e];
+#pragma unroll
+          for (int k = 1; k < W; ++k) z[e] += o_all[wave + k][lane][e];
+          z[e] *= inv;
+        }
+        if constexpr (E == 1) {
+          dst[0] = (uint16_t)f32_to_bf16_rne(z[0]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(z[e], z[e + 1]);
+        }
+      }
+      if constexpr (W > 1) __syncthreads();
     }
-    if (split == 0 && out.count && threadIdx.x % 16 == 0) out.count[out.at(a, 0, t, hq)] = splits;
   }
 }
 
@@ -542,6 +742,22 @@ __global__ __launch_bounds__(64 * kFewWaves, few_occupancy(D, NT)) void k_kv_att
 // tokens into LDS in operand order while the products of this step run; two buffers, one barrier
 // a step. Bound: matrix and vector issue alike (exponentials, conversions).
 
+// How the kernel cuts: tokens of a split, most splits.
+struct KvSplit {
+  int C, S;
+};
+// Partial results of split rows in the workspace: unscaled sums o [S][T][Hq][D] with their maximum
+// and sum of weights ml [S][T][Hq], and in how many splits a row is, count [T][Hq] (1: the row is
+// in the output already, as a row of the other kernel's is). All null where nothing is split.
+struct KvParts {
+  float* o;
+  float2* ml;
+  int32_t* count;
+  __device__ __forceinline__ int64_t at(const KvAttnArgs& a, int split, int t, int hq) const {
+    return ((int64_t)split * a.T + t) * a.Hq + hq;
+  }
+};
+
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
 typedef float v16f __attribute__((ext_vector_type(16)));
 
@@ -555,7 +771,13 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
   RowTile w;
   // last tiles first: with a causal mask they see the most tokens
   if (!find_row_tile(a, kManyRows, (int)(gridDim.x / S / a.H - 1 - blockIdx.x / S / a.H), w)) return;
-  if (w.n * a.G < rows_least) return;  // the other kernel's
+  if (w.n * a.G < rows_least) {  // the other kernel's
+    if (split == 0 && out.count && (int)threadIdx.x < w.rows) {
+      const int r = w.rb + (int)threadIdx.x;
+      out.count[out.at(a, 0, w.q0 + r / a.G, h * a.G + r % a.G)] = 1;
+    }
+    return;
+  }
   const int splits = splits_of(w, C, S);
   if (split >= splits) return;
 
@@ -640,11 +862,11 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
       const uint8_t* blk = (lane & 16) ? b1 : b0;
       const int in_page = (lane & 16) ? in1 : in0;
       const uint8_t* kc = blk + in_page * (8 * D) + half * 256 + (lane & 15) * 16;
-      const uint8_t* kb = blk + P * D + in_page * (D / 2) + half * 16 + (lane & 15);
+      const uint8_t* kb = blk + P * D + in_page * (D / 2) + half * 16 + (lane & 12);
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
         k[x][c] = *reinterpret_cast<const u32x4*>(kc + c * 512);
-        ks[x][c] = kb[c * 32];
+        ks[x][c] = *reinterpret_cast<const uint32_t*>(kb + c * 32);
       }
     }
   };
@@ -704,9 +926,9 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
           const v8i kv = {(int)k[x][c].x, (int)k[x][c].y, (int)k[x][c].z, (int)k[x][c].w, 0, 0, 0, 0};
-          s[x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_hi[c], s[x], 4, 0, 0, (int)ks[x][c], 0, (int)q_sc);
-          s[x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_lo[c], s[x], 4, 0, 0, (int)ks[x][c], 0,
-                                                                 (int)(q_sc - 5u));
+          const int sc = (int)(ks[x][c] >> (8 * (lane & 3)));  // the product takes its low byte
+          s[x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_hi[c], s[x], 4, 0, 0, sc, 0, (int)q_sc);
+          s[x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_lo[c], s[x], 4, 0, 0, sc, 0, (int)(q_sc - 5u));
         }
       }
     }
@@ -800,16 +1022,14 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
   if (split == 0 && out.count && half == 0) out.count[at] = splits;
 }
 
-// Joins the splits: W waves (1 or 4) per row and query head, each every W-th split, added in a
-// fixed order. Which rows are split, and in how many, is read with the maxima: two dependent
-// loads to the first sums.
-template <int D, int W>
+// Joins the splits of the many-rows kernel, a wave a row and query head. Whether a row is split,
+// and in how many, is read with the maxima: two dependent loads to the first sums.
+template <int D>
 __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvParts in) {
   constexpr int E = D / 64;
-  __shared__ float o_all[4][D];
-  __shared__ float l_all[4];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, part = W == 1 ? 0 : wave;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x, each = (int64_t)a.T * a.Hq;
+  typedef float vec __attribute__((ext_vector_type(E)));
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), each = (int64_t)a.T * a.Hq;
+  const int lane = threadIdx.x & 63;
   if (row >= each) return;
   const int t = (int)(row / a.Hq), hq = (int)(row % a.Hq);
   if (t < a.cu_q[0] || t >= a.cu_q[a.B]) return;  // no request's
@@ -821,26 +1041,14 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvPar
   for (int s = lane; s < splits; s += 64) m = fmaxf(m, in.ml[s * each + row].x);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  typedef float vec __attribute__((ext_vector_type(E)));
-#pragma unroll 8
-  for (int s = part; s < splits; s += W) {
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
     const float2 ml = in.ml[s * each + row];
     const vec y = *reinterpret_cast<const vec*>(in.o + (s * each + row) * D + lane * E);
     const float f = __builtin_amdgcn_exp2f(ml.x - m);
     l += ml.y * f;
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] += y[e] * f;
-  }
-  if constexpr (W == 4) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) o_all[wave][lane * E + e] = x[e];
-    if (lane == 0) l_all[wave] = l;
-    __syncthreads();
-    if (wave != 0) return;
-    l = ((l_all[0] + l_all[1]) + l_all[2]) + l_all[3];
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      x[e] = ((o_all[0][lane * E + e] + o_all[1][lane * E + e]) + o_all[2][lane * E + e]) + o_all[3][lane * E + e];
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint16_t* dst = a.out + (int64_t)t * a.out_stride + hq * D + lane * E;
@@ -854,89 +1062,110 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvPar
 
 // ------------------------------------------------------------------------------- the launch
 
+constexpr int64_t kWorkers = 512, kManySegments = 1024, kWholeWorkers = 1 << 14, kLeastUnits = 4, kWholeTokens = 1280;
+constexpr int64_t kManyGroups = 2048, kLeastTokens = 512;
+
 // Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not
 // launched), the others in the many-rows kernel (rows_most == kAllRows: not launched).
 struct KvPlan {
   int rows_most;
-  KvSplit few, many;
+  int R, lg;  // few rows: rows of a tile, log2 of the workers
+  bool cut;   // whether shares cut segments, and if so
+  int parts, row_groups;  // how many parts a long segment has, fours of rows in a tile
+  KvSplit many;
 };
 
-size_t part_bytes(const KvAttnSizes& z, int64_t S) {
-  return S <= 1 ? 0 : (size_t)(z.T * z.Hq * (S * (z.D + 2) + 1) * 4);
+size_t few_bytes(const KvAttnSizes& z, const KvPlan& p) {
+  return p.rows_most > 0 && p.cut ? ((size_t)1 << p.lg) * (2 * p.R * (z.D + 2) * 4 + 16) : 0;
 }
-
-// Splits of one kernel whose row tiles see `span` tokens at most: enough of them that `groups`
-// busy workgroups become `wanted`, at least `least` tokens each. launched: row tiles and heads of
-// the launch, of which many may have nothing to do.
-void split_tokens(KvSplit& k, int64_t span, int64_t groups, int64_t launched, int64_t wanted, int64_t least,
-                  int64_t multiple) {
-  const int64_t S = std::max<int64_t>(1, std::min(wanted / std::max<int64_t>(groups, 1), ((int64_t)1 << 20) / launched));
-  const int64_t C = std::max(least, (span + S - 1) / S);
-  k.C = (int)((C + multiple - 1) / multiple * multiple);
-  k.S = (int)std::max<int64_t>(1, (span + k.C - 1) / k.C);
+size_t many_bytes(const KvAttnSizes& z, const KvPlan& p) {
+  return p.rows_most < kAllRows && p.many.S > 1 ? (size_t)(z.T * z.Hq * (p.many.S * (z.D + 2) + 1) * 4) : 0;
 }
 
 KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   KvPlan p;
   const int64_t G = z.Hq / z.H, max_q = std::min(z.max_q, z.T), rows = max_q * G, few_rows = z.D == 256 ? 16 : 32;
-  p.few.R = rows <= 16 || (rows > few_rows && G <= 16) || z.D == 256 ? 16 : 32;
-  p.many.R = kManyRows;
-  const bool few_fit = (z.T * G / p.few.R + z.B) * z.H <= (1 << 20);
-  if (rows <= few_rows && few_fit) p.rows_most = kAllRows;
-  else if (z.T == z.B * max_q || !few_fit) p.rows_most = 0;  // every request has max_q rows
-  else p.rows_most = p.few.R;
+  p.R = rows <= 16 || (rows > few_rows && G <= 16) || z.D == 256 ? 16 : 32;
+  if (rows <= few_rows) p.rows_most = kAllRows;
+  else if (z.T == z.B * max_q) p.rows_most = 0;  // every request has max_q rows
+  else p.rows_most = p.R;
   const int64_t longest = std::min(z.max_kv, (int64_t)1 << 30);
-  auto span = [&](int R) { return z.window ? std::min(longest, z.window + R / G + 16) : longest; };
-  const int64_t few_tiles = p.rows_most == kAllRows ? std::max(z.B * ((rows + p.few.R - 1) / p.few.R), z.T * G / p.few.R) : z.B;
-  split_tokens(p.few, span(p.few.R), z.H * few_tiles, z.H * (z.T * G / p.few.R + z.B), 2048, 256, 128);
-  split_tokens(p.many, span(p.many.R), z.H * std::max<int64_t>(z.T * G / kManyRows, 1), z.H * row_tiles(z, kManyRows), 2048,
-               512, 64);
-  if (p.rows_most == kAllRows) p.many.S = 1;
-  if (p.rows_most == 0) p.few.S = 1;
-  if (part_bytes(z, std::max(p.few.S, p.many.S)) > workspace_bytes) {
-    p.few.C = p.many.C = 1 << 30;
-    p.few.S = p.many.S = 1;
+  auto span = [&](int64_t R) { return z.window ? std::min(longest, z.window + R / G + 16) : longest; };
+
+  // few rows
+  const int64_t segments = z.H * z.B * (p.rows_most == kAllRows ? (rows + p.R - 1) / p.R : 1);
+  const int64_t units = segments * ((span(p.R) + 31) / 32 + kSegmentUnits);
+  p.cut = span(p.R) > kWholeTokens;
+  const int64_t most = segments < kManySegments ? kWorkers : 2 * kWorkers;
+  const int64_t workers = p.cut ? std::min<int64_t>(most, units / kLeastUnits) : std::min<int64_t>(kWholeWorkers, segments);
+  for (p.lg = 0; ((int64_t)2 << p.lg) <= workers; ++p.lg) {
   }
+  if (!p.cut && ((int64_t)1 << p.lg) < workers) ++p.lg;
+
+  p.parts = (int)(((int64_t)1 << p.lg) / std::max<int64_t>(segments, 1)) + 1;
+  p.row_groups = (int)((std::min<int64_t>(rows, p.R) + 3) / 4);
+
+  // many rows: enough splits that the groups with rows become kManyGroups, at least kLeastTokens each
+  const int64_t tiles = z.H * std::max<int64_t>(z.T * G / kManyRows, 1), launched = z.H * row_tiles(z, kManyRows);
+  const int64_t S = std::max<int64_t>(1, std::min(kManyGroups / tiles, ((int64_t)1 << 20) / launched));
+  p.many.C = (int)((std::max<int64_t>(kLeastTokens, (span(kManyRows) + S - 1) / S) + 63) / 64 * 64);
+  p.many.S = (int)std::max<int64_t>(1, (span(kManyRows) + p.many.C - 1) / p.many.C);
+
+  if (few_bytes(z, p) + many_bytes(z, p) > workspace_bytes) p.many = {1 << 30, 1};
+  if (few_bytes(z, p) > workspace_bytes) p.cut = false;
   return p;
 }
 
 template <int D>
 hipError_t launch(const KvAttnArgs& a, const KvAttnSizes& z, const KvPlan& p, void* ws, hipStream_t st) {
-  const int S = std::max(p.few.S, p.many.S);
-  const size_t each = (size_t)a.T * a.Hq;
-  KvParts parts = {nullptr, nullptr, nullptr};
-  if (S > 1) {
-    parts.o = static_cast<float*>(ws);
-    parts.ml = reinterpret_cast<float2*>(parts.o + S * each * D);
-    parts.count = reinterpret_cast<int32_t*>(parts.ml + S * each);
-  }
   hipError_t e = hipSuccess;
   if (p.rows_most > 0) {
-    const int64_t tiles = p.rows_most == kAllRows ? row_tiles(z, p.few.R) : z.B;
-    const dim3 grid((unsigned)(tiles * a.H * p.few.S)), block(64 * kFewWaves);
-    if (D == 256 || p.few.R == 16) hipLaunchKernelGGL((k_kv_attn_few<D, 1>), grid, block, 0, st, a, p.rows_most, p.few, parts);
-    else hipLaunchKernelGGL((k_kv_attn_few<D == 256 ? 64 : D, 2>), grid, block, 0, st, a, p.rows_most, p.few, parts);
+    const size_t slots = ((size_t)2 << p.lg) * p.R;
+    KvShares sh = {p.lg, p.rows_most, nullptr, nullptr, nullptr};
+    if (p.cut) {
+      sh.o = static_cast<float*>(ws);
+      sh.ml = reinterpret_cast<float2*>(sh.o + slots * D);
+      sh.seams = reinterpret_cast<int4*>(sh.ml + slots);
+    }
+    const dim3 grid(1u << p.lg), block(kThreads);
+    if (p.R == 16) hipLaunchKernelGGL((k_kv_attn_few<D, 1>), grid, block, 0, st, a, sh);
+    else hipLaunchKernelGGL((k_kv_attn_few<D == 256 ? 64 : D, 2>), grid, block, 0, st, a, sh);  // R is 16 at D = 256
     e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (p.cut) {
+      // many parts: few segments, so of eight neighbouring workers one or two have a seam at most
+      const unsigned workers = 1u << p.lg;
+      if (p.parts > 12)
+        hipLaunchKernelGGL((k_kv_attn_seams<D, 4>), dim3((workers + 7) / 8, p.row_groups), dim3(1024), 0, st, a, sh, p.R, 8);
+      else
+        hipLaunchKernelGGL((k_kv_attn_seams<D, 1>), dim3(workers, p.row_groups), dim3(256), 0, st, a, sh, p.R, 1);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
-  if (e == hipSuccess && p.rows_most < kAllRows) {
+  if (p.rows_most < kAllRows) {
+    const size_t each = (size_t)a.T * a.Hq;
+    KvParts parts = {nullptr, nullptr, nullptr};
+    if (p.many.S > 1) {
+      parts.o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + few_bytes(z, p));
+      parts.ml = reinterpret_cast<float2*>(parts.o + p.many.S * each * D);
+      parts.count = reinterpret_cast<int32_t*>(parts.ml + p.many.S * each);
+    }
     const dim3 grid((unsigned)((int64_t)row_tiles(z, kManyRows) * a.H * p.many.S)), block(64 * kManyWaves);
     hipLaunchKernelGGL((k_kv_attn_many<D>), grid, block, 0, st, a, p.rows_most + 1, p.many, parts);
     e = hipGetLastError();
+    if (e != hipSuccess || p.many.S == 1) return e;
+    hipLaunchKernelGGL((k_kv_attn_join<D>), dim3((unsigned)((each + 3) / 4)), dim3(256), 0, st, a, p.many.S, parts);
+    e = hipGetLastError();
   }
-  if (e != hipSuccess || S == 1) return e;
-  // four waves a row where there are many splits to add and few rows to fill the chip
-  if (S > 8 && each <= 4096)
-    hipLaunchKernelGGL((k_kv_attn_join<D, 4>), dim3((unsigned)each), dim3(256), 0, st, a, S, parts);
-  else
-    hipLaunchKernelGGL((k_kv_attn_join<D, 1>), dim3((unsigned)((each + 3) / 4)), dim3(256), 0, st, a, S, parts);
-  return hipGetLastError();
+  return e;
 }
 
 }  // namespace
 
 size_t kv_attn_workspace_bytes(const KvAttnSizes& z) {
   const KvPlan p = plan_of(z, ~(size_t)0);
-  return part_bytes(z, std::max(p.few.S, p.many.S));
+  return few_bytes(z, p) + many_bytes(z, p);
 }
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, const KvAttnSizes& z, void* workspace, size_t workspace_bytes,
@@ -953,13 +1182,14 @@ void kv_attn_plan(const KvAttnSizes& z, size_t workspace_bytes, char* buf, size_
     return;
   }
   const KvPlan p = plan_of(z, workspace_bytes);
-  char few[64] = "", many[64] = "";
+  char few[96] = "", many[96] = "";
   if (p.rows_most > 0)
-    std::snprintf(few, sizeof few, "k_kv_attn_few<%d, %d> C=%d S=%d", (int)z.D, p.few.R / 16, p.few.C, p.few.S);
+    std::snprintf(few, sizeof few, "k_kv_attn_few<%d, %d> workers=%d%s", (int)z.D, p.R / 16, 1 << p.lg,
+                  p.cut ? " + k_kv_attn_seams" : "");
   if (p.rows_most < kAllRows)
-    std::snprintf(many, sizeof many, "k_kv_attn_many<%d> C=%d S=%d", (int)z.D, p.many.C, p.many.S);
-  std::snprintf(buf, len, "%s%s%s%s", few, few[0] && many[0] ? " + " : "", many,
-                p.few.S > 1 || p.many.S > 1 ? " + k_kv_attn_join" : "");
+    std::snprintf(many, sizeof many, "k_kv_attn_many<%d> C=%d S=%d%s", (int)z.D, p.many.C, p.many.S,
+                  p.many.S > 1 ? " + k_kv_attn_join" : "");
+  std::snprintf(buf, len, "%s%s%s", few, few[0] && many[0] ? " + " : "", many);
 }
 
 }  // namespace mx

@@ -278,6 +278,23 @@ def test_attention_of_few_rows(D, H, G, page, q, kv):
     c.check(mx, workspace=False, what="no workspace")
 
 
+@pytest.mark.parametrize("B", [257, 700])
+def test_attention_of_many_requests(B):
+    """More requests than a workgroup has threads, ragged, some empty, alone and beside a chunk."""
+    torch_or_skip()
+    mx = lib_or_fail()
+    rng = np.random.default_rng(B)
+    kv = rng.integers(0, 90, B)
+    kv[B // 2] = 5000
+    c = Case(64, 1, 2, 16, [1] * B, kv, seed=B)
+    c.check(mx, what="decode")
+    c.check(mx, workspace=False, what="no workspace")
+    q = rng.integers(0, 3, B)
+    q[B - 1], kv[B - 1] = 60, 200
+    c = Case(64, 1, 2, 16, q, kv, seed=B + 1, extra_rows=1)
+    c.check(mx, what="mixed")
+
+
 # prompts and chunks: D, H, G, page, row counts, kv lengths
 MANY = [
     (64, 1, 1, 16, [33], [33]), (128, 1, 1, 16, [64, 65, 1], [64, 65, 100]), (256, 1, 1, 16, [40], [300]),

@@ -130,12 +130,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
 
 // l + the two bf16 values of a word: the sum of the weights as the product with V takes them.
 __device__ __forceinline__ float add_pair(float l, uint32_t u) {
-  return l + (__builtin_bit_cast(float, u << 16) + __builtin_bit_cast(float, u & 0xFFFF0000u));
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, u), __builtin_bit_cast(bf16x2, 0x3F803F80u), l, false);
 }
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8, (u32x4){a, b, c, d});
+}
+
+// What lies at a device address that was put together from its halves.
+template <typename T>
+__device__ __forceinline__ T global(uint64_t at) {
+  return *(const __attribute__((address_space(1))) T*)at;
 }
 
 // Byte I of a word (a pair of codes) times its scale, the scale byte J of another word.
@@ -818,11 +824,10 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
       }
   }
 
-  // tokens: the workgroup's, and those that some row of the wave sees
+  // the workgroup's tokens, and where those end that some row of the wave sees
   const int t0 = w.lo + split * C;
   const int t1 = split == S - 1 ? w.hi : min(w.hi, t0 + C);
   const int tiles = (t1 - t0 + 15) >> 4, steps = (tiles + 3) >> 2;
-  const int wave_lo = row_begin(a, w.pos(first, a.G));
   const int wave_hi = wave_rows > 0 ? row_end(a, w.len, w.pos(last, a.G)) : 0;
   const int all_lo = row_begin(a, w.pos(last, a.G)), all_hi = min(t1, row_end(a, w.len, w.pos(first, a.G)));
   const float c2 = a.scale * kLog2e;
@@ -831,52 +836,62 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
   const int P = 1 << a.log2_page;
   const int32_t* table = a.block_table + (int64_t)w.b * a.max_blocks;
 
-  // pages of 64 token tiles, one a lane, for the current group of 64 and the next; -1: hidden
-  auto pages_of_group = [&](int grp) {
-    const int tile = 64 * grp + lane;
-    int id = -1;
-    if (tile < tiles) {
-      id = table[(t0 + 16 * tile) >> a.log2_page];
-      if (id < 0 || id >= a.num_pages) id = -1;
-    }
-    return id;
+  // Where 64 token tiles lie, one a lane: the window from tile 32 window on, moved every eight
+  // steps, its pages fetched eight steps before. codes: the tile's K codes; scales: from there to
+  // its K scales. V's codes and scales lie P D / 2 and P M past those. Tiles past the last repeat it.
+  auto page_of = [&](int window) { return table[(t0 + 16 * clamp_int(32 * window + lane, 0, max(tiles - 1, 0))) >> a.log2_page]; };
+  int window = 0, page = 0, next_page = 0, to_scales = 0;
+  uint32_t codes_lo = 0, codes_hi = 0;
+  uint64_t hidden_tiles = 0;
+  auto place = [&]() {
+    const bool bad = page < 0 || page >= a.num_pages;
+    hidden_tiles = __ballot(bad);
+    const int in_page = ((t0 + 16 * clamp_int(32 * window + lane, 0, max(tiles - 1, 0))) & (P - 1)) >> 4;
+    const int64_t at = ((int64_t)(bad ? 0 : page) * a.H + h) * a.block_bytes + in_page * (8 * D);
+    const uint64_t codes = (uint64_t)(uintptr_t)a.cache + (uint64_t)at;
+    codes_lo = (uint32_t)codes;
+    codes_hi = (uint32_t)(codes >> 32);
+    to_scales = P * D - in_page * (8 * D - D / 2);
   };
-  int group = 0, page0 = pages_of_group(0), page1 = pages_of_group(1);
-  auto page_at = [&](int tile) {  // tile in the current group or the next
-    return __builtin_amdgcn_readlane((tile >> 6) == group ? page0 : page1, tile & 63);
-  };
-  auto block_at = [&](int tile, int& in_page) {
-    tile = min(tile, tiles - 1);
-    in_page = ((t0 + 16 * tile) & (P - 1)) >> 4;
-    return a.cache + ((int64_t)max(page_at(tile), 0) * a.H + h) * a.block_bytes;
-  };
+  auto lane_of = [&](uint32_t x, int tile) { return (uint32_t)__builtin_amdgcn_readlane((int)x, tile - 32 * window); };
 
   u32x4 k[2][KC];
   uint32_t ks[2][KC];
-  auto load_k = [&](int step) {
+  auto load_k = [&](int step, auto X) {  // half X of a step: 32 tokens
+    constexpr int x = X;
+    const int tile = 4 * step + 2 * x;
+    const uint32_t lo0 = lane_of(codes_lo, tile), lo1 = lane_of(codes_lo, tile + 1), hi0 = lane_of(codes_hi, tile),
+                   hi1 = lane_of(codes_hi, tile + 1), to0 = lane_of((uint32_t)to_scales, tile),
+                   to1 = lane_of((uint32_t)to_scales, tile + 1);
+    const bool second = lane & 16;
+    const uint64_t codes = (uint64_t)(second ? hi1 : hi0) << 32 | (second ? lo1 : lo0);
+    const uint64_t kc = codes + (uint32_t)(half * 256 + (lane & 15) * 16);
+    const uint64_t kb = codes + ((second ? to1 : to0) + half * 16 + (lane & 12));
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      int in0, in1;
-      const uint8_t* b0 = block_at(4 * step + 2 * x, in0);
-      const uint8_t* b1 = block_at(4 * step + 2 * x + 1, in1);
-      const uint8_t* blk = (lane & 16) ? b1 : b0;
-      const int in_page = (lane & 16) ? in1 : in0;
-      const uint8_t* kc = blk + in_page * (8 * D) + half * 256 + (lane & 15) * 16;
-      const uint8_t* kb = blk + P * D + in_page * (D / 2) + half * 16 + (lane & 12);
+    for (int c = 0; c < KC; ++c) {
+      k[x][c] = global<u32x4>(kc + c * 512);
+      ks[x][c] = global<uint32_t>(kb + c * 32);
+    }
+  };
+  auto scores = [&](v16f& s, auto X) {
+    constexpr int x = X;
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        k[x][c] = *reinterpret_cast<const u32x4*>(kc + c * 512);
-        ks[x][c] = *reinterpret_cast<const uint32_t*>(kb + c * 32);
-      }
+    for (int e = 0; e < 16; ++e) s[e] = 0.f;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      const v8i kv = {(int)k[x][c].x, (int)k[x][c].y, (int)k[x][c].z, (int)k[x][c].w, 0, 0, 0, 0};
+      const int sc = (int)(ks[x][c] >> (8 * (lane & 3)));  // the product takes its low byte
+      s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_hi[c], s, 4, 0, 0, sc, 0, (int)q_sc);
+      s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_lo[c], s, 4, 0, 0, sc, 0, (int)(q_sc - 5u));
     }
   };
   typedef uint32_t words __attribute__((ext_vector_type(M)));
   words v, vs;  // the wave's token tile of a step: as in TokenTile
   auto load_v = [&](int step) {
-    int in_page;
-    const uint8_t* blk = block_at(4 * step + wave, in_page);
-    v = *reinterpret_cast<const words*>(blk + P * (D / 2) + in_page * (8 * D) + lane * (4 * M));
-    vs = *reinterpret_cast<const words*>(blk + P * D + P * M + in_page * (16 * M) + (lane >> 4) * (4 * M));
+    const int tile = 4 * step + wave;
+    const uint64_t codes = (uint64_t)lane_of(codes_hi, tile) << 32 | lane_of(codes_lo, tile);
+    v = global<words>(codes + (uint32_t)(P * (D / 2)) + (uint32_t)lane * (4u * M));
+    vs = global<words>(codes + (lane_of((uint32_t)to_scales, tile) + P * M) + ((uint32_t)lane >> 4) * (4u * M));
   };
   auto decode_v = [&](int step, int buf) {
     const int tile = 4 * step + wave, t = t0 + 16 * tile;
@@ -886,7 +901,7 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
       x.v[j] = v[j];
       x.vs[j] = vs[j];
     }
-    const bool hidden = tile >= tiles || page_at(min(tile, tiles - 1)) < 0;
+    const bool hidden = (hidden_tiles >> (tile - 32 * window)) & 1u;
     if (t + 16 > t1 || hidden) x.mask(t + 4 * (lane >> 4), w.lo, hidden ? 0 : t1);
     uint2* dst = reinterpret_cast<uint2*>(&v_lds[buf][wave][0][((lane >> 4) & 1) * 32 + (lane & 15)]) + (lane >> 5);
     static_for<M>([&](auto J) {
@@ -907,58 +922,47 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[j][e] = 0.f;
 
+  // Half a step at a time: the scores of the next half are in the matrix pipe while this half's
+  // weights are worked out, and the next step's values are decoded under this step's products.
+  constexpr std::integral_constant<int, 0> H0{};
+  constexpr std::integral_constant<int, 1> H1{};
+  v16f s0, s1;
   if (steps > 0) {
+    page = page_of(0);
+    next_page = page_of(1);
+    place();
     load_v(0);
-    load_k(0);
+    load_k(0, H0);
+    load_k(0, H1);
     decode_v(0, 0);
     load_v(1);
+    scores(s0, H0);
+    load_k(1, H0);
   }
   __syncthreads();
   for (int st = 0; st < steps; ++st) {
     const int t = t0 + 64 * st;
-    const bool mine = t < wave_hi && t + 64 > wave_lo;  // else no row of the wave sees any of it
-    v16f s[2];
-    if (mine) {
+    if ((st >> 3) != window) {
+      ++window;
+      page = next_page;
+      next_page = page_of(window + 1);
+      place();
+    }
+    const uint32_t hidden = (uint32_t)(hidden_tiles >> (4 * st - 32 * window)) & 15u;
+    const bool masked = t < all_lo || t + 64 > all_hi || hidden;
+    // The maximum of a half's scores, and the sums rescaled if it passes the one in use by kLag.
+    auto settle = [&](v16f& s, auto X) {
+      constexpr int x = X;
+      if (masked) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[x][e] = 0.f;
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const v8i kv = {(int)k[x][c].x, (int)k[x][c].y, (int)k[x][c].z, (int)k[x][c].w, 0, 0, 0, 0};
-          const int sc = (int)(ks[x][c] >> (8 * (lane & 3)));  // the product takes its low byte
-          s[x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_hi[c], s[x], 4, 0, 0, sc, 0, (int)q_sc);
-          s[x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kv, q_lo[c], s[x], 4, 0, 0, sc, 0, (int)(q_sc - 5u));
+        for (int e = 0; e < 16; ++e) {
+          const int tok = t + 32 * x + 8 * (e / 4) + 4 * half + e % 4;
+          if (tok < row_lo || tok >= min(row_hi, t1) || ((hidden >> (2 * x + e / 8)) & 1u)) s[e] = -INFINITY;
         }
       }
-    }
-    uint32_t hidden = 0;
+      float top = s[0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) hidden |= page_at(min(4 * st + i, tiles - 1)) < 0 ? 1u << i : 0u;
-    if (st + 1 < steps) {
-      load_k(st + 1);
-      decode_v(st + 1, (st + 1) & 1);
-      if (((4 * (st + 1)) >> 6) != group) {  // the next step begins the next group of tiles
-        page0 = page1;
-        page1 = pages_of_group(++group + 1);
-      }
-      load_v(st + 2);
-    }
-    if (mine) {
-      if (t < all_lo || t + 64 > all_hi || hidden) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int tok = t + 32 * x + 8 * (e / 4) + 4 * half + e % 4;
-            if (tok < row_lo || tok >= min(row_hi, t1) || ((hidden >> (2 * x + e / 8)) & 1u)) s[x][e] = -INFINITY;
-          }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
       top *= c2;
       if (__any(top > m + kLag)) {  // as in the kernel above
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -970,26 +974,53 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[j][e] *= alpha;
       }
-      uint32_t p[2][8];
+    };
+    uint32_t p[8];
+    auto weights = [&](const v16f& s) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const uint32_t u = pack_bf16(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x][e], c2, -m)),
-                                       __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][e + 1], c2, -m)));
-          p[x][e / 2] = u;
-          l = add_pair(l, u);
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8 pt = as_bf16x8(p[i / 2][4 * (i % 2)], p[i / 2][4 * (i % 2) + 1], p[i / 2][4 * (i % 2) + 2],
-                                    p[i / 2][4 * (i % 2) + 3]);
-#pragma unroll
-        for (int j = 0; j < M; ++j) {
-          const bf16x8 vt = __builtin_bit_cast(bf16x8, v_lds[st & 1][i][j][lane]);
-          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt, pt, o[j], 0, 0, 0);
-        }
+      for (int e = 0; e < 16; e += 2) {
+        p[e / 2] = pack_bf16(__builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c2, -m)),
+                             __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + 1], c2, -m)));
+        l = add_pair(l, p[e / 2]);
       }
+    };
+    // A half's values leave LDS before its weights are worked out: read where they are used, every
+    // product waits for them.
+    bf16x8 vt[2][M];
+    auto fetch = [&](auto X) {
+      constexpr int x = X;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < M; ++j) vt[i][j] = __builtin_bit_cast(bf16x8, v_lds[st & 1][2 * x + i][j][lane]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto values = [&]() {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bf16x8 pt = as_bf16x8(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+#pragma unroll
+        for (int j = 0; j < M; ++j) o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt[i][j], pt, o[j], 0, 0, 0);
+      }
+    };
+    if (t < wave_hi) {  // else no row of the wave sees this or a later step
+      settle(s0, H0);
+      fetch(H0);
+      scores(s1, H1);
+      weights(s0);
+      load_k(st + 1, H1);
+      values();
+      settle(s1, H1);
+      fetch(H1);
+      scores(s0, H0);
+      weights(s1);
+      load_k(st + 2, H0);
+      decode_v(st + 1, (st + 1) & 1);
+      load_v(st + 2);
+      values();
+    } else {
+      decode_v(st + 1, (st + 1) & 1);
+      load_v(st + 2);
     }
     __syncthreads();
   }

@@ -75,6 +75,39 @@ __device__ __forceinline__ bool find_row_tile(const KvAttnArgs& a, int R, int ti
 }
 int row_tiles(const KvAttnSizes& z, int R) { return (int)(z.T * (z.Hq / z.H) / R + z.B); }
 
+// The same with the tiles of the requests that see the most tokens first, each request's last tile
+// (with a causal mask its longest) first: what is long is not left for the end. Up to 64 requests,
+// one a lane: each counts those before it, and the tiles are summed in that order. Past 64 the
+// order stays the requests', last tiles first.
+__device__ __forceinline__ bool find_row_tile_longest(const KvAttnArgs& a, int R, int tile, int launched, RowTile& w) {
+  if (a.B > 64) return find_row_tile(a, R, launched - 1 - tile, w);
+  const int lane = threadIdx.x & 63;
+  int tiles = 0, seen = -1;
+  if (lane < a.B) {
+    const int q0 = clamp_int(a.cu_q[lane], 0, a.T), n = clamp_int(a.cu_q[lane + 1], q0, a.T) - q0;
+    const int len = (int)min((int64_t)max(a.kv_lens[lane], 0), (int64_t)a.max_blocks << a.log2_page);
+    tiles = (n * a.G + R - 1) / R;
+    seen = a.window ? min(len, a.window) : len;
+  }
+  int before = 0;
+  for (int b = 0; b < a.B; ++b) {
+    const int other = __builtin_amdgcn_readlane(seen, b);
+    before += other > seen || (other == seen && b < lane);
+  }
+  if (lane >= a.B) before = lane;
+  const int own = __builtin_amdgcn_ds_permute(before * 4, tiles), request = __builtin_amdgcn_ds_permute(before * 4, lane);
+  int upto = own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(upto, d);
+    if (lane >= d) upto += y;
+  }
+  const uint64_t at = __ballot(tile < upto && tile >= upto - own);
+  if (at == 0) return false;
+  const int k = __builtin_ctzll(at);
+  return row_tile_of(a, R, __builtin_amdgcn_readlane(request, k), (__builtin_amdgcn_readlane(upto, k) - 1 - tile) * R, w);
+}
+
 // The tokens [lo, hi) of a row tile in splits of C; the last of at most S takes what is left.
 __device__ __forceinline__ int splits_of(const RowTile& w, int C, int S) {
   return clamp_int((w.hi - w.lo + C - 1) / C, 1, S);
@@ -773,10 +806,11 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
   constexpr int M = D / 32, KC = D / 64;
   __shared__ uint4 v_lds[2][4][M][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, half = lane >> 5;
-  const int C = cut.C, S = cut.S, split = (int)(blockIdx.x % S), h = (int)(blockIdx.x / S % a.H);
+  // Splits apart, then tiles, then heads: neighbours in the launch, which go to the eight XCDs in
+  // turn, have like work (a split that only long requests have would load every second XCD).
+  const int C = cut.C, S = cut.S, groups = (int)(gridDim.x / S), split = (int)(blockIdx.x / groups), h = (int)(blockIdx.x % a.H);
   RowTile w;
-  // last tiles first: with a causal mask they see the most tokens
-  if (!find_row_tile(a, kManyRows, (int)(gridDim.x / S / a.H - 1 - blockIdx.x / S / a.H), w)) return;
+  if (!find_row_tile_longest(a, kManyRows, (int)(blockIdx.x % groups / a.H), groups / a.H, w)) return;
   if (w.n * a.G < rows_least) {  // the other kernel's
     if (split == 0 && out.count && (int)threadIdx.x < w.rows) {
       const int r = w.rb + (int)threadIdx.x;
@@ -1025,32 +1059,61 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
     __syncthreads();
   }
 
-  if (32 * wave + col >= w.rows) return;
+  // Out through LDS (the wave's quarter of the values' place), so that a row's bytes are stored
+  // side by side: a row of D bf16, or half a row of FP32 sums at a time, in pieces of 16 bytes whose
+  // order in LDS depends on the row (all rows' first pieces would meet in one bank).
   l += __shfl_xor(l, 32);
+  constexpr int kPieces = D / 8;
+  uint4* mine = reinterpret_cast<uint4*>(v_lds) + wave * 32 * kPieces;
   const int t = w.q0 + r / a.G, hq = h * a.G + r % a.G;
-  const float inv = splits > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
   const int64_t at = out.at(a, split, t, hq);
+  if (32 * wave + col < w.rows && half == 0) {
+    if (splits > 1) out.ml[at] = make_float2(m, l);
+    if (split == 0 && out.count) out.count[at] = splits;
+  }
+  const float inv = splits > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+  uint8_t* row_out = splits > 1 ? reinterpret_cast<uint8_t*>(out.o + at * D)
+                                : reinterpret_cast<uint8_t*>(a.out + (int64_t)t * a.out_stride + hq * D);
+  const uint64_t row_at = (uint64_t)(uintptr_t)row_out;
+  auto put = [&](int piece, uint4 u) { mine[col * kPieces + (piece ^ (col & (kPieces - 1)))] = u; };
+  auto store = [&](int byte) {  // rows whose pieces the wave has put, to `byte` of each
+    __syncthreads();
 #pragma unroll
-  for (int j = 0; j < M; ++j)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[2 * e] = o[j][4 * x + e] * inv;
-        f[2 * e + 1] = o[j][8 + 4 * x + e] * inv;
-      }
-      const int d = 32 * j + 16 * x + 8 * half;
-      if (splits == 1) {
-        *reinterpret_cast<uint4*>(a.out + (int64_t)t * a.out_stride + hq * D + d) =
-            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-      } else {
-        *reinterpret_cast<v4f*>(out.o + at * D + d) = (v4f){f[0], f[1], f[2], f[3]};
-        *reinterpret_cast<v4f*>(out.o + at * D + d + 4) = (v4f){f[4], f[5], f[6], f[7]};
-      }
+    for (int i = 0; i < kPieces / 2; ++i) {
+      const int row = (64 * i + lane) / kPieces, piece = lane % kPieces;
+      const uint64_t to = (uint64_t)(uint32_t)__shfl((int)(row_at >> 32), row) << 32 | (uint32_t)__shfl((int)row_at, row);
+      const uint4 u = mine[row * kPieces + (piece ^ (row & (kPieces - 1)))];
+      if (32 * wave + row < w.rows) *(__attribute__((address_space(1))) u32x4*)(to + byte + 16 * piece) = (u32x4){u.x, u.y, u.z, u.w};
     }
-  if (splits > 1 && half == 0) out.ml[at] = make_float2(m, l);
-  if (split == 0 && out.count && half == 0) out.count[at] = splits;
+    __syncthreads();
+  };
+  if (splits == 1) {
+#pragma unroll
+    for (int j = 0; j < M; ++j)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t f[4];  // elements 32 j + 16 x + 8 half on: even ones from rows 0 .. 15 of V^T, odd ones from 16 on
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = pack_bf16(o[j][4 * x + e] * inv, o[j][8 + 4 * x + e] * inv);
+        put(4 * j + 2 * x + half, make_uint4(f[0], f[1], f[2], f[3]));
+      }
+    store(0);
+  } else {
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+#pragma unroll
+      for (int j = 0; j < M / 2; ++j)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const v16f& y = o[part * (M / 2) + j];
+            const v4f z = {y[4 * x + e], y[8 + 4 * x + e], y[4 * x + e + 1], y[8 + 4 * x + e + 1]};
+            put(8 * j + 4 * x + 2 * half + e / 2, __builtin_bit_cast(uint4, z));
+          }
+      store(part * 2 * D);
+    }
+  }
 }
 
 // Joins the splits of the many-rows kernel, a wave a row and query head. Whether a row is split,
@@ -1094,7 +1157,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvPar
 // ------------------------------------------------------------------------------- the launch
 
 constexpr int64_t kWorkers = 512, kManySegments = 1024, kWholeWorkers = 1 << 14, kLeastUnits = 4, kWholeTokens = 1280;
-constexpr int64_t kManyGroups = 2048, kLeastTokens = 512;
+constexpr int64_t kManySlots = 512, kLeastTokens = 512;
 
 // Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not
 // launched), the others in the many-rows kernel (rows_most == kAllRows: not launched).
@@ -1136,11 +1199,13 @@ KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   p.parts = (int)(((int64_t)1 << p.lg) / std::max<int64_t>(segments, 1)) + 1;
   p.row_groups = (int)((std::min<int64_t>(rows, p.R) + 3) / 4);
 
-  // many rows: enough splits that the groups with rows become kManyGroups, at least kLeastTokens each
+  // Many rows: as many splits as the groups with rows leave room for on the chip (kManySlots of them
+  // run at once, half as many at D = 256), at least kLeastTokens each.
   const int64_t tiles = z.H * std::max<int64_t>(z.T * G / kManyRows, 1), launched = z.H * row_tiles(z, kManyRows);
-  const int64_t S = std::max<int64_t>(1, std::min(kManyGroups / tiles, ((int64_t)1 << 20) / launched));
-  p.many.C = (int)((std::max<int64_t>(kLeastTokens, (span(kManyRows) + S - 1) / S) + 63) / 64 * 64);
-  p.many.S = (int)std::max<int64_t>(1, (span(kManyRows) + p.many.C - 1) / p.many.C);
+  const int64_t slots = z.D == 256 ? kManySlots / 2 : kManySlots, seen = span(kManyRows);
+  const int64_t S = std::max<int64_t>(1, std::min({slots / tiles, seen / kLeastTokens, ((int64_t)1 << 20) / launched}));
+  p.many.C = (int)((seen + 64 * S - 1) / (64 * S) * 64);
+  p.many.S = (int)std::max<int64_t>(1, (seen + p.many.C - 1) / p.many.C);
 
   if (few_bytes(z, p) + many_bytes(z, p) > workspace_bytes) p.many = {1 << 30, 1};
   if (few_bytes(z, p) > workspace_bytes) p.cut = false;

@@ -181,30 +181,107 @@ bool one_group(int64_t B, int64_t T_max) { return B <= kOneGroupRequests && T_ma
 
 // ------------------------------------------------------------------------------- write, read
 
-// One thread per 32-block of one head of one row: the library's block quantizer, its 16 code
-// bytes and its scale byte, for the key and for the value.
+// The largest bf16 exponent field of 8 elements.
+__device__ __forceinline__ uint32_t top_field(const uint4& u) {
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[i] & 0x7F807F80u));
+  return (uint32_t)(m.x > m.y ? m.x : m.y) >> 7;
+}
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+// 8 elements' codes at a block's scale byte: as quant_block, a scale byte of 0 is passed as 2^-127.
+__device__ __forceinline__ uint32_t quant8(const uint4& x, uint32_t s) {
+  const float sc = __builtin_bit_cast(float, s ? s << 23 : 0x00400000u);
+  uint32_t r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0, __builtin_bit_cast(bf16x2, x.x), sc, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x.y), sc, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x.z), sc, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x.w), sc, 3);
+}
+
+// A workgroup quantizes 16 kPasses rows of 128 elements (two heads of 64, a head of 128 or half a
+// head of 256): a thread has 8 elements of a row at a time, four neighbours a block. K's codes go
+// out as they come, 16 bytes a block. V's lie four tokens to a word in the cache: its bytes meet in
+// LDS, and wherever four rows of the workgroup are the four tokens of a word, whatever row the
+// first of them is, whole words are written; other rows' bytes one by one.
+// Bound: HBM, 4 bytes read and 17/16 written per element of K and V.
+template <int kPasses>
 __global__ __launch_bounds__(256) void k_kv_write(const uint16_t* __restrict__ k, int64_t k_stride,
                                                   const uint16_t* __restrict__ v, int64_t v_stride,
-                                                  const int64_t* __restrict__ slots, int64_t units,
+                                                  const int64_t* __restrict__ slots, int64_t T,
                                                   uint8_t* __restrict__ cache, int64_t num_slots, int lg, int heads,
                                                   int D) {
-  const int m = D / 32, per = heads * m;
+  constexpr int kRows = 16 * kPasses;
+  __shared__ uint32_t v_words[kRows][17];  // a row's 16 words of codes (one more spreads rows over the banks)
+  __shared__ int64_t row_slot[kRows];      // -1: writes nothing
   const KvLayout L = {1 << lg, D};
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-    const int64_t t = u / per;
-    const int h = (int)(u % per) / m, d = (int)(u % m) * 32;
-    const int64_t slot = slots[t];
-    if (slot < 0 || slot >= num_slots) continue;
-    const int tok = (int)(slot & (L.P - 1));
-    uint8_t* blk = cache + ((slot >> lg) * heads + h) * L.block_bytes();
-    uint32_t x[16], q[4];
-    load_block(k + t * k_stride + h * D + d, x);
-    blk[L.k_scale(tok, d)] = (uint8_t)quant_block(x, q);
-    *reinterpret_cast<uint4*>(blk + L.k_code(tok, d)) = make_uint4(q[0], q[1], q[2], q[3]);
-    load_block(v + t * v_stride + h * D + d, x);
-    blk[L.v_scale(tok, d)] = (uint8_t)quant_block(x, q);
+  const int m = D / 32, c = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int e = (int)blockIdx.y * 128 + 8 * c, h = e / D, d = e % D;  // this thread's 8 elements of a row
+  const bool has = h < heads;
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < T; t0 += (int64_t)gridDim.x * kRows) {
+    uint4 kx[kPasses], vx[kPasses];
+    int64_t slot[kPasses];
 #pragma unroll
-    for (int b = 0; b < 16; ++b) blk[L.v_code(tok, d + 2 * b)] = (uint8_t)(q[b / 4] >> (8 * (b % 4)));
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t t = t0 + 16 * i + group;
+      slot[i] = t < T ? slots[t] : -1;
+      if (slot[i] >= num_slots) slot[i] = -1;
+      kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
+      if (has && slot[i] >= 0) {
+        kx[i] = *reinterpret_cast<const uint4*>(k + t * k_stride + e);
+        vx[i] = *reinterpret_cast<const uint4*>(v + t * v_stride + e);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      uint32_t top = top_field(kx[i]) | top_field(vx[i]) << 16;  // both largest exponents
+      top = max_halves(top, (uint32_t)__shfl_xor((int)top, 1));
+      top = max_halves(top, (uint32_t)__shfl_xor((int)top, 2));
+      const uint32_t ek = top & 0xFFFFu, ev = top >> 16, sk = ek > 2u ? ek - 2u : 0u, sv = ev > 2u ? ev - 2u : 0u;
+      v_words[16 * i + group][c] = quant8(vx[i], sv);
+      if (c == 0) row_slot[16 * i + group] = slot[i];
+      if (has && slot[i] >= 0) {
+        const int tok = (int)(slot[i] & (L.P - 1));
+        uint8_t* blk = cache + ((slot[i] >> lg) * heads + h) * L.block_bytes();
+        *reinterpret_cast<uint32_t*>(blk + L.k_code(tok, d)) = quant8(kx[i], sk);
+        if ((c & 3) == 0) {
+          blk[L.k_scale(tok, d)] = (uint8_t)sk;
+          blk[L.v_scale(tok, d)] = (uint8_t)sv;
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {  // V's codes, row by row: the first of four tokens writes for all
+      const int r = kPasses * group + i;
+      const int64_t s = row_slot[r];
+      if (!has || s < 0) continue;
+      const int at = (int)(s & 3), first = r - at;
+      bool four = first >= 0 && first + 3 < kRows;
+      if (four)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) four = four && row_slot[first + x] == s - at + x;
+      const int tok = (int)(s & (L.P - 1));
+      uint8_t* blk = cache + ((s >> lg) * heads + h) * L.block_bytes();
+      if (!four) {
+        const uint32_t w = v_words[r][c];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) blk[L.v_code(tok, d + 2 * b)] = (uint8_t)(w >> (8 * b));
+      } else if (at == 0) {
+        // bytes of four tokens, transposed: word b gets byte b of each
+        const uint32_t w0 = v_words[r][c], w1 = v_words[r + 1][c], w2 = v_words[r + 2][c], w3 = v_words[r + 3][c];
+        const uint32_t a = __builtin_amdgcn_perm(w1, w0, 0x05010400), b = __builtin_amdgcn_perm(w3, w2, 0x05010400);
+        const uint32_t p = __builtin_amdgcn_perm(w1, w0, 0x07030602), q = __builtin_amdgcn_perm(w3, w2, 0x07030602);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(blk + L.v_code(tok, d));
+        dst[0] = __builtin_amdgcn_perm(b, a, 0x05040100);
+        dst[m] = __builtin_amdgcn_perm(b, a, 0x07060302);
+        dst[2 * m] = __builtin_amdgcn_perm(q, p, 0x05040100);
+        dst[3 * m] = __builtin_amdgcn_perm(q, p, 0x07060302);
+      }
+    }
+    __syncthreads();  // before the next rows take their place
   }
 }
 
@@ -267,11 +344,16 @@ hipError_t launch_kv_tables(const KvTablesArgs& a, void* workspace, hipStream_t 
 hipError_t launch_kv_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slots,
                            int64_t T, void* cache, int64_t num_pages, int64_t P, int64_t heads, int64_t D,
                            hipStream_t st) {
-  const int64_t units = T * heads * (D / 32);
   const int lg = __builtin_ctzll((unsigned long long)P);
-  hipLaunchKernelGGL(k_kv_write, dim3(groups_of(units)), dim3(256), 0, st,
-                     static_cast<const uint16_t*>(k), k_stride, static_cast<const uint16_t*>(v), v_stride, slots, units,
-                     static_cast<uint8_t*>(cache), num_pages * P, lg, (int)heads, (int)D);
+  // few rows: more workgroups of one pass; many: 64 rows, so that 60 or more of them are whole words' rows
+  const int rows = T <= 1024 ? 16 : 64;
+  const dim3 grid((unsigned)min((T + rows - 1) / rows, (int64_t)1 << 20), (unsigned)((heads * D + 127) / 128));
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, static_cast<const uint16_t*>(k), k_stride,
+                       static_cast<const uint16_t*>(v), v_stride, slots, T, static_cast<uint8_t*>(cache), num_pages * P, lg,
+                       (int)heads, (int)D);
+  };
+  if (rows == 16) launch(k_kv_write<1>); else launch(k_kv_write<4>);
   return hipGetLastError();
 }
 

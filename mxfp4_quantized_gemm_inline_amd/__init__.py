@@ -469,16 +469,20 @@ def _new(shape, dtype, like, stream):
 
 
 def _meta(t, name, dtype, least=0):
-    """The checks of _need that the cache calls use, once per tensor: a decoding step makes a few
-    of these calls per layer, with up to ten tensors each."""
+    """The checks of _need that the cache calls use, in one pass: a decoding step makes a few of
+    these calls per layer, with up to ten tensors each."""
+    try:
+        if t.dtype is dtype and t.numel() >= least and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() < least:
         raise ValueError(f"{name} holds {t.numel()} elements, needs at least {least}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows3(t, name):
@@ -497,21 +501,20 @@ def _rows3(t, name):
     return T, H, D, row if T > 1 else H * D
 
 
-def _pointers(**tensors):
+def _pointers(names, *tensors):
     """Device pointers of tensors whose metadata was checked (None stays None): all of them on
-    the current device."""
-    current, out = None, []
-    for name, t in tensors.items():
+    the current device. names: theirs, in one string."""
+    current = _torch().cuda.current_device() if tensors[0].is_cuda else None
+    out = []
+    for i, t in enumerate(tensors):
         if t is None:
             out.append(None)
             continue
-        index = t.get_device()
-        if index < 0:
-            raise ValueError(f"{name} must be a device tensor")
-        if current is None:
-            current = _torch().cuda.current_device()
-        if index != current:
-            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{current}")
+        if t.get_device() != current:
+            name = names.split()[i]
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a device tensor")
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{_torch().cuda.current_device()}")
         out.append(t.data_ptr())
     return out
 
@@ -562,8 +565,8 @@ def mx_kv_tables(old_lens, new_lens, block_table, free_pages, free_count, page_s
     else:
         workspace = None
     old_, new_, table_, stack_, count_, out_, cu_, slots_, pos_, status_, ws_ = _pointers(
-        old_lens=old_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, free_count=free_count,
-        free_count_out=free_count_out, cu_q=cu_q, slots=slots, positions=positions, status=status, workspace=workspace)
+        "old_lens new_lens block_table free_pages free_count free_count_out cu_q slots positions status workspace", old_lens,
+        new_lens, block_table, free_pages, free_count, free_count_out, cu_q, slots, positions, status, workspace)
     _check(lib().mx_kv_tables(old_, new_, B, int(page_size), table_, max_blocks, stack_, free_pages.numel(), count_, out_,
                               max_rows, cu_, slots_, pos_, status_, ws_, ws_bytes, _stream_ptr(stream)), "mx_kv_tables")
     return cu_q, slots, positions, free_count_out, status
@@ -581,7 +584,7 @@ def mx_kv_write(k_bf16, v_bf16, slots, cache, page_size: int, stream=None) -> No
     pages = _kv_pages(cache, page_size, heads, D)
     if T == 0:
         return
-    k_, v_, slots_, cache_ = _pointers(k_bf16=k_bf16, v_bf16=v_bf16, slots=slots, cache=cache)
+    k_, v_, slots_, cache_ = _pointers("k_bf16 v_bf16 slots cache", k_bf16, v_bf16, slots, cache)
     _check(lib().mx_kv_write(k_, k_stride, v_, v_stride, slots_, T, cache_, pages, int(page_size), heads, D,
                              _stream_ptr(stream)), "mx_kv_write")
 
@@ -601,7 +604,7 @@ def mx_kv_read(cache, slots, heads: int, D: int, page_size: int, k_out=None, v_o
             raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if shape[0] == 0:
         return k, v
-    cache_, slots_, k_, v_ = _pointers(cache=cache, slots=slots, k_out=k, v_out=v)
+    cache_, slots_, k_, v_ = _pointers("cache slots k_out v_out", cache, slots, k, v)
     _check(lib().mx_kv_read(cache_, pages, int(page_size), shape[1], shape[2], slots_, shape[0], k_, v_,
                             _stream_ptr(stream)), "mx_kv_read")
     return k, v
@@ -655,8 +658,8 @@ def mx_kv_attention(q_bf16, cache, block_table, cu_q, kv_lens, heads: int, page_
     if workspace is not None:
         _meta(workspace, "workspace", workspace.dtype)
         ws_bytes = workspace.numel() * workspace.element_size()
-    q_, cache_, table_, cu_, kv_, out_, ws_ = _pointers(q_bf16=q_bf16, cache=cache, block_table=block_table, cu_q=cu_q,
-                                                        kv_lens=kv_lens, out=out, workspace=workspace)
+    q_, cache_, table_, cu_, kv_, out_, ws_ = _pointers(
+        "q_bf16 cache block_table cu_q kv_lens out workspace", q_bf16, cache, block_table, cu_q, kv_lens, out, workspace)
     _check(lib().mx_kv_attention(q_, q_stride, cache_, pages, page_size, table_, max_blocks, cu_, kv_, B, T, heads_q, heads,
                                  D, max_q, max_kv, 1 if causal else 0, window, scale, out_, out_stride, ws_, ws_bytes,
                                  _stream_ptr(stream)), "mx_kv_attention")

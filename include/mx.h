@@ -337,7 +337,7 @@ size_t mx_kv_cache_bytes(int64_t num_pages, int64_t page_size, int64_t heads, in
  * it twice with the same arguments gives the same result. A page must stand on the stack or
  * in the table's held entries once. workspace: mx_kv_tables_workspace_bytes(B, T_max) bytes
  * (0 for small batches: NULL), 16-byte aligned. Requires 0 <= B <= 2^20, 1 <= max_blocks,
- * 0 <= T_max <= 2^30, 0 <= capacity < 2^31 and page_size as above. Errors: MX_ERR_NULL,
+ * max_blocks * page_size <= 2^30, 0 <= T_max <= 2^30, 0 <= capacity < 2^31 and page_size as above. Errors: MX_ERR_NULL,
  * MX_ERR_SHAPE, MX_ERR_ALIGN (4 bytes; slots 8; workspace 16), MX_ERR_WORKSPACE,
  * MX_ERR_DEVICE, MX_ERR_HIP.
  */
@@ -389,12 +389,14 @@ mx_status mx_kv_read(const void* cache, int64_t num_pages, int64_t page_size, in
  *    and nothing else (any value >= 1 is correct).
  *  workspace: partial results where the tokens of a request are split over the chip, of
  *    mx_kv_attention_workspace_bytes(...) bytes; always optional: with a NULL or smaller one
- *    the tokens are split less or not at all.
- * Queries are used exactly (not quantized); scores and the softmax's maximum and sum are
- * FP32; the weights are rounded to bf16 for the product with V, whose sum is FP32; the result
- * is rounded once. Output is bitwise reproducible for the same arguments. Requires 0 <= T <=
- * 2^30 / heads_q, 0 <= B <= 2^22 / heads (and 2^20), 1 <= max_blocks, scale finite and > 0, |scale * q . K| below 1e38 and
- * the cache's sizes as above. T == 0 or B == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE,
+ *    the tokens are split less or not at all. Calls that may overlap need one each; nothing in
+ *    it needs clearing.
+ * Queries are not quantized (a row is used exactly down to 2^-21 of its largest element);
+ * scores and the softmax's maximum and sum are FP32; the weights are rounded to bf16 for the
+ * product with V, whose sum is FP32; the result is rounded once. Output is bitwise reproducible
+ * for the same arguments. Requires 0 <= T <= 2^30 / heads_q, heads_q <= 1024, 0 <= B <= 2^22 /
+ * heads (and 2^20), 1 <= max_blocks, max_blocks * page_size <= 2^30, scale finite and > 0,
+ * |scale * q . K| below 1e38 and the cache's sizes as above. T == 0 or B == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE,
  * MX_ERR_ALIGN (q, out, cache, workspace: 16 bytes; tables: 4), MX_ERR_DEVICE, MX_ERR_HIP.
  */
 mx_status mx_kv_attention(const void* q_bf16, int64_t q_stride, const void* cache, int64_t num_pages,

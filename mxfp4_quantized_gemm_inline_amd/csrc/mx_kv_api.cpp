@@ -14,12 +14,12 @@ constexpr int64_t kMaxStride = int64_t(1) << 32;  // elements: rows times stride
 constexpr int64_t kMaxPages = int64_t(1) << 31;
 constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxTiles = int64_t(1) << 22;   // requests times heads: a launch holds under 2^32 threads
-constexpr int64_t kMaxTokens = int64_t(1) << 31;  // of one request: positions are 32-bit
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of one request: positions stay in 32 bits, also past a tile's end
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool page_ok(int64_t P) { return P >= 16 && P <= 1024 && (P & (P - 1)) == 0; }
 bool head_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
-bool table_ok(int64_t max_blocks, int64_t P) { return max_blocks >= 1 && max_blocks <= (kMaxTokens - 1) / P; }
+bool table_ok(int64_t max_blocks, int64_t P) { return max_blocks >= 1 && max_blocks <= kMaxTokens / P; }
 bool stride_ok(int64_t s, int64_t least) { return s >= least && s < kMaxStride && s % 8 == 0; }
 int log2_of(int64_t P) { return __builtin_ctzll((unsigned long long)P); }
 mx_status from_hip(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_HIP; }

@@ -15,8 +15,11 @@ namespace mx {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLag = 8.f;
 constexpr float kLowest = -3.0e38f;  // the running maximum before any token: below every score
+// How far, in powers of two, the maximum in use may lag behind the true one before the sums are
+// rescaled: weights reach 2^8 then, which neither bf16's relative rounding nor an FP32 sum feels,
+// and the rescaling of all sums is left out of nearly every step.
+constexpr float kLag = 8.f;
 
 // ------------------------------------------------------------------------------- row tiles
 //
@@ -1184,7 +1187,8 @@ KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   else if (z.T == z.B * max_q) p.rows_most = 0;  // every request has max_q rows
   else p.rows_most = p.R;
   const int64_t longest = std::min(z.max_kv, (int64_t)1 << 30);
-  auto span = [&](int64_t R) { return z.window ? std::min(longest, z.window + R / G + 16) : longest; };
+  // tokens that a tile of R rows sees at most
+  auto span = [&](int64_t R) { return z.window && z.window < longest ? std::min(longest, z.window + R / G + 16) : longest; };
 
   // few rows
   const int64_t segments = z.H * z.B * (p.rows_most == kAllRows ? (rows + p.R - 1) / p.R : 1);

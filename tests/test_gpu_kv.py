@@ -161,6 +161,32 @@ def test_write_bytes_match_the_oracle(T, H, D, page, layout, order):
         assert np.all(g[gone] == 7.0)
 
 
+def test_write_of_a_slot_named_twice_stays_in_its_slot():
+    """The documentation leaves open whose bytes it holds; no other slot's byte changes."""
+    torch_or_skip()
+    mx = lib_or_fail()
+    T, H, D, page = 70, 2, 64, 16
+    k, v = W.normal_bf16((T, H, D), seed=5), W.normal_bf16((T, H, D), seed=6)
+    slots = np.arange(T, dtype=np.int64)
+    slots[[9, 33, 66]] = 40                                # and 40 itself
+    start = np.random.default_rng(7).integers(0, 256, (6, H, KV.block_bytes(page, D)), dtype=np.uint8)
+    cache = dev(start)
+    mx.mx_kv_write(dev_bf16(k), dev_bf16(v), dev(slots), cache, page)
+    got = cache.cpu().numpy()
+    keep = np.setdiff1d(np.arange(T), [9, 33, 66, 40])
+    want = start.copy()
+    KV.write(want, k[keep], v[keep], slots[keep], page)
+    own = np.zeros(start.shape[2], dtype=bool)             # the bytes of slot 40 in its page
+    tok = 40 % page
+    for j in range(D // 32):
+        own[[KV.byte_of(kind, page, D, tok, j) for kind in ("ks", "vs")]] = True
+        for b in range(16):
+            own[[KV.byte_of(kind, page, D, tok, j, b) for kind in ("k", "v")]] = True
+    same = got == want
+    same[40 // page, :, own] = True
+    assert same.all()
+
+
 def test_cache_past_32_bit_offsets():
     """A cache of 4.6 GB: pages whose bytes lie past 2^31 and 2^32."""
     torch = torch_or_skip()
@@ -402,6 +428,35 @@ def test_attention_extreme_values():
         blk[:, KV.byte_of("vs", P, D, tok % P, 1)] = 127 + 100
         blk[:, KV.byte_of("vs", P, D, tok % P, 2)] = 10
     c.check(mx, what="V scales")
+
+
+def test_attention_of_shared_pages():
+    """Requests that share the pages of a common beginning, and one page twice in a request."""
+    torch_or_skip()
+    mx = lib_or_fail()
+    for q in ([1, 1, 2], [40, 1, 50]):
+        c = Case(128, 2, 2, 16, q, [100, 90, 120], seed=21)
+        c.table[1, :4] = c.table[0, :4]
+        c.table[2, 3] = c.table[2, 1]
+        c.check(mx, what="shared")
+
+
+def test_attention_calls_at_the_same_time():
+    """Two streams, each with its own workspace and output, many calls in flight."""
+    torch = torch_or_skip()
+    mx = lib_or_fail()
+    cases = [Case(128, 2, 4, 16, [1, 1, 1], [3000, 1700, 40], seed=22), Case(128, 1, 2, 16, [100, 3], [2500, 800], seed=23)]
+    want = [c.check(mx) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    inputs = [(dev_bf16(c.q), c.args(), dict(max_q=max(c.q_lens), max_kv=max(c.kv_lens))) for c in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(12):
+        for i, (q, args, kw) in enumerate(inputs):
+            outs[i].append(mx.mx_kv_attention(q, *args, stream=streams[i], **kw))
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert all(np.array_equal(host_bits(o), w) for o in got)
 
 
 def test_attention_strided_rows_and_output():

@@ -30,7 +30,7 @@ def test_tables_argument_errors():
     base = dict(old=A, new=B, B=4, page=16, table=C, blocks=8, stack=D_, capacity=10, count=E, count_out=F, rows=8, cu=A,
                 slots=B, pos=C, flag=D_, ws=None, ws_bytes=0, stream=None)
     for k, v in (("B", -1), ("B", (1 << 20) + 1), ("page", 15), ("page", 48), ("page", 2048), ("blocks", 0),
-                 ("blocks", 1 << 28), ("capacity", -1), ("capacity", 1 << 31), ("rows", -1), ("rows", (1 << 30) + 1)):
+                 ("blocks", (1 << 26) + 1), ("capacity", -1), ("capacity", 1 << 31), ("rows", -1), ("rows", (1 << 30) + 1)):
         _call("mx_kv_tables", base, mx.MX_ERR_SHAPE, **{k: v})
     for k in ("old", "new", "table", "stack", "count", "count_out", "cu", "slots", "pos", "flag"):
         _call("mx_kv_tables", base, mx.MX_ERR_NULL, **{k: None})
@@ -70,7 +70,7 @@ def test_attention_argument_errors():
     base = dict(q=A, qs=1024, cache=B, pages=9, page=16, table=C, blocks=4, cu=D_, kv=E, B=2, T=5, Hq=8, H=2, D=128, max_q=3,
                 max_kv=60, causal=1, window=0, scale=0.1, out=F, os=1024, ws=None, ws_bytes=0, stream=None)
     for k, v in (("qs", 1020), ("qs", -8), ("os", 1016), ("os", 1028), ("pages", 0), ("page", 17), ("blocks", 0),
-                 ("blocks", 1 << 27), ("B", -1), ("B", (1 << 20) + 1), ("T", -1), ("T", 1 << 30), ("Hq", 9), ("Hq", 0),
+                 ("blocks", (1 << 26) + 1), ("B", -1), ("B", (1 << 20) + 1), ("T", -1), ("T", 1 << 30), ("Hq", 9), ("Hq", 0),
                  ("H", 0), ("D", 96), ("max_q", 0), ("max_kv", 0), ("causal", 2), ("window", -1), ("scale", 0.0),
                  ("scale", -1.0), ("scale", float("nan")), ("scale", float("inf"))):
         _call("mx_kv_attention", base, mx.MX_ERR_SHAPE, **{k: v})
@@ -87,6 +87,32 @@ def test_attention_argument_errors():
     with pytest.raises(mx.MxError):
         mx.mx_kv_attention_plan(2, 5, 9, 2, 128, 1, 64)
     assert mx.lib().mx_kv_attention_plan(2, 5, 8, 2, 128, 1, 64, 0, 0, None, 0) == mx.MX_ERR_NULL
+
+
+def test_attention_plan_follows_rows_and_lengths():
+    plan, ws = mx.mx_kv_attention_plan, mx.mx_kv_attention_workspace_bytes
+    # decoding: equal shares of the tokens, more of them where there are many segments
+    assert plan(64, 64, 64, 8, 128, 1, 8192) == "k_kv_attn_few<128, 1> workers=512 + k_kv_attn_seams"
+    assert plan(512, 512, 64, 8, 128, 1, 2048) == "k_kv_attn_few<128, 1> workers=1024 + k_kv_attn_seams"
+    assert ws(64, 64, 64, 8, 128, 1, 8192) == 512 * (2 * 16 * (128 + 2) * 4 + 16)
+    # short segments, also by a window, stay whole, one a worker and more
+    assert plan(32, 128, 12, 12, 64, 4, 4001, 1024) == "k_kv_attn_few<64, 1> workers=512"
+    assert plan(256, 256, 64, 8, 128, 1, 700) == "k_kv_attn_few<128, 1> workers=2048"
+    assert ws(256, 256, 64, 8, 128, 1, 700) == 0
+    # up to 32 rows beside each other, 16 at D = 256
+    assert plan(4, 16, 32, 4, 128, 4, 100).startswith("k_kv_attn_few<128, 2>")
+    assert plan(4, 16, 32, 4, 256, 4, 100) == "k_kv_attn_many<256> C=128 S=1"
+    # whole prompts fill the chip; few tiles over a long cache are split
+    assert plan(1, 8192, 32, 8, 128, 8192, 8192) == "k_kv_attn_many<128> C=8192 S=1"
+    assert plan(1, 512, 32, 8, 128, 512, 16000) == "k_kv_attn_many<128> C=4032 S=4 + k_kv_attn_join"
+    assert ws(1, 512, 32, 8, 128, 512, 16000) == 512 * 32 * (4 * 130 + 1) * 4
+    # rows of both kinds: each kernel its own; without the workspace neither cuts
+    assert plan(20, 1553, 32, 4, 128, 512, 4096) == ("k_kv_attn_few<128, 1> workers=512 + k_kv_attn_seams + "
+                                                     "k_kv_attn_many<128> C=4096 S=1")
+    assert plan(20, 1553, 32, 4, 128, 512, 4096, workspace_bytes=0) == ("k_kv_attn_few<128, 1> workers=512 + "
+                                                                       "k_kv_attn_many<128> C=1073741824 S=1")
+    for hint in (1, 10 ** 6, 2 ** 62):
+        assert plan(3, 7, 8, 2, 64, hint, hint, 2 ** 62) != ""
 
 
 def test_binding_checks_metadata():

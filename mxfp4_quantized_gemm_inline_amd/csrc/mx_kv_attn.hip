@@ -702,10 +702,12 @@ __global__ __launch_bounds__(256 * W) void k_kv_attn_seams(KvAttnArgs a, KvShare
   typedef float vec __attribute__((ext_vector_type(E)));
   __shared__ vec o_all[4 * W][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wave % W;
-  const int first = (int)blockIdx.x * each;
-  for (int worker = first; worker < min(first + each, 1 << sh.lg); ++worker) {
+  const int first = (int)blockIdx.x * each, own = first + lane;
+  uint64_t with_seam = __ballot(lane < each && own < (1 << sh.lg) && sh.seams[min(own, (1 << sh.lg) - 1)].w != 0);
+  for (; with_seam; with_seam &= with_seam - 1) {
+    const int worker = first + __builtin_ctzll(with_seam);
     const int4 seam = sh.seams[worker];
-    const int parts = seam.w & 0x3FFFFFFF, rows = parts ? seam.z >> 16 : 0, h = seam.z & 0xFFFF;
+    const int parts = seam.w & 0x3FFFFFFF, rows = seam.z >> 16, h = seam.z & 0xFFFF;
     for (int r0 = 4 * (int)blockIdx.y; r0 < rows; r0 += 4 * (int)gridDim.y) {
       const int r = r0 + wave / W;
       float l = 0.f;
@@ -1159,7 +1161,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvPar
 
 // ------------------------------------------------------------------------------- the launch
 
-constexpr int64_t kWorkers = 512, kManySegments = 1024, kWholeWorkers = 1 << 14, kLeastUnits = 4, kWholeTokens = 1280;
+constexpr int64_t kWorkers = 512, kManySegments = 1024, kWholeWorkers = 1 << 14, kLeastUnits = 12, kWholeTokens = 1280;
 constexpr int64_t kManySlots = 512, kLeastTokens = 512;
 
 // Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not

@@ -124,29 +124,25 @@ __device__ __forceinline__ int splits_of(const RowTile& w, int C, int S) {
 // largest and to 2^-21 of it below. So the keys enter the scaled MFMA as they lie in the cache,
 // 4-bit with their scale bytes, and none is ever converted; one product more pays for that with
 // the same matrix time as bf16 and no vector time.
-__device__ __forceinline__ void split_fp8(const uint32_t (&x)[8], float down, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+__device__ __forceinline__ void split_fp8(const uint32_t (&x)[8], uint32_t scale, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  // the conversions divide by, or multiply with, a power of two
+  const float by = __builtin_bit_cast(float, scale << 23), by_lo = __builtin_bit_cast(float, (scale - 5u) << 23);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float f[4], r[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f[2 * i] = __builtin_bit_cast(float, x[2 * j + i] << 16) * down;
-      f[2 * i + 1] = __builtin_bit_cast(float, x[2 * j + i] & 0xFFFF0000u) * down;
-    }
-    uint32_t h = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-    h = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], h, true);
-    r[0] = (f[0] - __builtin_amdgcn_cvt_f32_fp8(h, 0)) * 32.f;
-    r[1] = (f[1] - __builtin_amdgcn_cvt_f32_fp8(h, 1)) * 32.f;
-    r[2] = (f[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 32.f;
-    r[3] = (f[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 32.f;
-    uint32_t l = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
-    l = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], l, true);
-    hi[j] = h;
-    lo[j] = l;
+    const uint32_t a = x[2 * j], b = x[2 * j + 1];
+    s16x2 h = {0, 0}, l = {0, 0};
+    h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(bf16x2, a), by, false);
+    h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(bf16x2, b), by, true);
+    hi[j] = __builtin_bit_cast(uint32_t, h);
+    const f32x2 p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi[j], by, false), q = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi[j], by, true);
+    l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, __builtin_bit_cast(float, a << 16) - p.x, __builtin_bit_cast(float, a & 0xFFFF0000u) - p.y, by_lo, false);
+    l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, __builtin_bit_cast(float, b << 16) - q.x, __builtin_bit_cast(float, b & 0xFFFF0000u) - q.y, by_lo, true);
+    lo[j] = __builtin_bit_cast(uint32_t, l);
   }
 }
-// Scale byte of hi for a row whose largest exponent field is E (lo's is 5 less); the row is
-// multiplied by 2^(127 - byte) before it is split.
+// Scale byte of hi for a row whose largest exponent field is E (lo's is 5 less).
 __device__ __forceinline__ uint32_t query_scale(uint32_t E) { return E > 12u ? E - 7u : 5u; }
 
 // Largest exponent field of bf16 pairs.
@@ -279,13 +275,13 @@ constexpr int kAllRows = 0x7FFFFFFF;
 // output; of one that is cut, each worker leaves an unscaled part: in its slot 0 if the segment is
 // its first, else in its slot 1 (its last). The worker whose share begins in the second part of a
 // segment names the parts to the join.
-// Without a workspace a worker takes the whole segments that begin in its share.
+// Where every segment is short, or without a workspace, a workgroup takes one whole segment.
 constexpr int kSegmentUnits = 4;
 
 struct KvShares {
   int lg;         // log2 of the workers
   int rows_most;  // requests of more rows (query rows times group) are the other kernel's
-  float* o;       // [workers][2][R][D], or null: no segment is cut
+  float* o;       // [workers][2][R][D]
   float2* ml;     // [workers][2][R]: maximum, sum
   int4* seams;    // [workers]: first query row; first row of the tile; head | rows << 16; parts | slot of the first << 30
 };
@@ -312,93 +308,92 @@ __device__ __forceinline__ KvRequest request_of(const KvAttnArgs& a, int b, int 
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
-template <int D, int NT>
+template <int D, int NT, bool kShared>
 __global__ __launch_bounds__(kThreads, few_occupancy(D, NT)) void k_kv_attn_few(KvAttnArgs a, KvShares sh) {
   constexpr int R = 16 * NT, M = D / 32, KC = (D + 127) / 128, LD = D + 4;
   __shared__ float o_all[kWaves][16][LD];
   __shared__ float2 ml_all[kWaves][R];
-  __shared__ int64_t sums[kThreads + 1];  // units before each thread's requests
-  __shared__ KvRequest requests[kThreads];
+  __shared__ int64_t sums[kShared ? kThreads : 1];  // units before each thread's requests
+  __shared__ KvRequest requests[kShared ? kThreads : 1];
   __shared__ int64_t wave_sum[kWaves];
   __shared__ int found;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
-
-  // where the shares lie: a sum over the requests, each thread `per` of them
-  const int per = (a.B + kThreads - 1) / kThreads;
-  int64_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const KvRequest r = request_of(a, threadIdx.x * per + i, sh.rows_most);
-    if (i == 0) requests[threadIdx.x] = r;
-    if (r.n > 0) mine += (int64_t)r.tiles(a.G, R) * a.H * r.units(a);
-  }
-  int64_t upto = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t y = __shfl_up(upto, d);
-    if (lane >= d) upto += y;
-  }
-  if (lane == 63) wave_sum[wave] = upto;
-  __syncthreads();
-  int64_t W = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    if (i == wave) upto += W;
-    W += wave_sum[i];
-  }
-  int lg = sh.lg;
-  while (lg > 0 && (W >> lg) == 0) --lg;  // a unit a worker at least
-  const int worker = (int)blockIdx.x;
-  if (W == 0 || worker >> lg) {
-    if (threadIdx.x == 0 && sh.o) sh.seams[worker].w = 0;
-    return;
-  }
-  auto share_at = [&](int i) { return i * (W >> lg) + ((i * (W & (((int64_t)1 << lg) - 1))) >> lg); };  // i W / 2^lg
-  int64_t u = share_at(worker);
-  const int64_t u_end = share_at(worker + 1);
-  sums[threadIdx.x] = upto - mine;
-  if (threadIdx.x == kThreads - 1) sums[kThreads] = W;
-  if (upto - mine <= u && u < upto) found = threadIdx.x;
-  __syncthreads();
-  int b = __builtin_amdgcn_readfirstlane(found) * per;
-  int64_t before = sums[__builtin_amdgcn_readfirstlane(found)];  // units before request b
-
   const float c2 = a.scale * kLog2e;
   uint32_t shift = 23;
   asm volatile("" : "+v"(shift));  // kept in a register: scale_at
-  const int P = 1 << a.log2_page;
+  const int P = 1 << a.log2_page, worker = (int)blockIdx.x, per = (a.B + kThreads - 1) / kThreads;
+  int64_t W = 0, u = 0, u_end = 1, before = 0;
+  int lg = sh.lg, b = 0, h = worker % a.H;
+  RowTile w;
+  auto share_at = [&](int i) { return i * (W >> lg) + ((i * (W & (((int64_t)1 << lg) - 1))) >> lg); };  // i W / 2^lg
+
+  if constexpr (kShared) {
+    // where the shares lie: a sum over the requests, each thread `per` of them
+    int64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const KvRequest r = request_of(a, threadIdx.x * per + i, sh.rows_most);
+      if (i == 0) requests[threadIdx.x] = r;
+      if (r.n > 0) mine += (int64_t)r.tiles(a.G, R) * a.H * r.units(a);
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t y = __shfl_up(upto, d);
+      if (lane >= d) upto += y;
+    }
+    if (lane == 63) wave_sum[wave] = upto;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      if (i == wave) upto += W;
+      W += wave_sum[i];
+    }
+    while (lg > 0 && (W >> lg) == 0) --lg;  // a unit a worker at least
+    if (W == 0 || worker >> lg) {
+      if (threadIdx.x == 0) sh.seams[worker].w = 0;
+      return;
+    }
+    u = share_at(worker);
+    u_end = share_at(worker + 1);
+    sums[threadIdx.x] = upto - mine;
+    if (upto - mine <= u && u < upto) found = threadIdx.x;
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(found) * per;
+    before = sums[__builtin_amdgcn_readfirstlane(found)];  // units before request b
+  } else if (sh.rows_most == kAllRows) {
+    if (!find_row_tile(a, R, worker / a.H, w)) return;
+  } else if (!row_tile_of(a, R, worker / a.H, 0, w) || w.n * a.G > sh.rows_most) {  // a tile a request
+    return;
+  }
 
   for (bool first = true; u < u_end; first = false) {
-    // the segment of unit u
-    KvRequest req;
-    int units;
-    int64_t all;
-    for (;; ++b) {  // u < W: some request ends after it
-      req = per == 1 ? requests[b] : request_of(a, b, sh.rows_most);
-      units = __builtin_amdgcn_readfirstlane(req.units(a));
-      all = req.n > 0 ? (int64_t)req.tiles(a.G, R) * a.H * units : 0;
-      if (u < before + all) break;
-      before += all;
-    }
-    const int64_t in = u - before;
-    const int seg = (in >> 31) ? (int)(in / units) : (int)((uint32_t)in / (uint32_t)units);  // head fastest
-    const int from = (int)(in - (int64_t)seg * units), h = seg % a.H;
-    const int64_t seg_start = u - from, seg_end = seg_start + units;
-    RowTile w;
-    w.b = b;
-    w.q0 = __builtin_amdgcn_readfirstlane(req.q0);
-    w.n = __builtin_amdgcn_readfirstlane(req.n);
-    w.len = __builtin_amdgcn_readfirstlane(req.len);
-    w.rb = seg / a.H * R;
-    w.rows = min(R, w.n * a.G - w.rb);
-    w.lo = row_begin(a, w.pos(w.rb, a.G)) & ~15;
-    w.hi = row_end(a, w.len, w.pos(w.rb + w.rows - 1, a.G));
-    int t0 = w.lo, t1 = w.hi;
     bool whole = true;
-    if (sh.o) {
-      const int to = (int)(min(u_end, seg_end) - seg_start);
+    if constexpr (kShared) {
+      // the segment of unit u
+      KvRequest req;
+      int units;
+      for (;; ++b) {  // u < W: some request ends after it
+        req = per == 1 ? requests[b] : request_of(a, b, sh.rows_most);
+        units = __builtin_amdgcn_readfirstlane(req.units(a));
+        const int64_t all = req.n > 0 ? (int64_t)req.tiles(a.G, R) * a.H * units : 0;
+        if (u < before + all) break;
+        before += all;
+      }
+      const int64_t in = u - before;
+      const int seg = (in >> 31) ? (int)(in / units) : (int)((uint32_t)in / (uint32_t)units);  // head fastest
+      const int from = (int)(in - (int64_t)seg * units);
+      const int64_t seg_start = u - from, seg_end = seg_start + units;
+      h = seg % a.H;
+      w.b = b;
+      w.q0 = __builtin_amdgcn_readfirstlane(req.q0);
+      w.n = __builtin_amdgcn_readfirstlane(req.n);
+      w.len = __builtin_amdgcn_readfirstlane(req.len);
+      w.rb = seg / a.H * R;
+      w.rows = min(R, w.n * a.G - w.rb);
+      w.lo = row_begin(a, w.pos(w.rb, a.G)) & ~15;
+      w.hi = row_end(a, w.len, w.pos(w.rb + w.rows - 1, a.G));
+      const int to = (int)(min(u_end, seg_end) - seg_start), lo = w.lo;
       whole = from == 0 && to == units;
-      t0 = w.lo + 32 * max(from - kSegmentUnits, 0);
-      if (to < units) t1 = min(t1, w.lo + 32 * max(to - kSegmentUnits, 0));
       if (first && threadIdx.x == 0) {
         const int64_t u_before = share_at(worker - 1);
         int4 seam = make_int4(w.q0, w.rb, h | (w.rows << 16), 0);
@@ -412,16 +407,18 @@ __global__ __launch_bounds__(kThreads, few_occupancy(D, NT)) void k_kv_attn_few(
         }
         sh.seams[worker] = seam;
       }
-    } else if (from > 0) {  // begun in an earlier share
+      // the share's part of the tile's tokens; rows still see what they see
+      w.lo = lo + 32 * max(from - kSegmentUnits, 0);
+      if (to < units) w.hi = min(w.hi, lo + 32 * max(to - kSegmentUnits, 0));
       u = seg_end;
-      continue;
+    } else {
+      u = u_end;
     }
-    u = seg_end;
 
     // this wave's tokens
-    const int share = (max(t1 - t0, 0) + 32 * kWaves - 1) / (32 * kWaves) * 32;
-    const int w0 = t0 + wave * share, w1 = min(t1, w0 + share);
-    const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
+    const int share = (max(w.hi - w.lo, 0) + 32 * kWaves - 1) / (32 * kWaves) * 32;
+    const int w0 = w.lo + wave * share, w1 = min(w.hi, w0 + share);
+    const int32_t* table = a.block_table + (int64_t)w.b * a.max_blocks;
     int base = w0, tiles = 0, page = 0;
     uint64_t bad_tiles = 0;
     auto fetch_pages = [&]() {  // of 64 token tiles from base on, one a lane
@@ -493,13 +490,12 @@ __global__ __launch_bounds__(kThreads, few_occupancy(D, NT)) void k_kv_attn_few(
       E = max(E, (uint32_t)__shfl_xor((int)E, 16));
       E = max(E, (uint32_t)__shfl_xor((int)E, 32));
       const uint32_t sc = query_scale(E);
-      const float down = __builtin_bit_cast(float, (254u - sc) << 23);
       if constexpr (D == 64) {
         // one 16x16x128 product takes both parts: k < 64 is hi (bytes 0..15), k >= 64 lo, over the
         // same keys given twice (lane groups 2 and 3 load what 0 and 1 do)
         const uint32_t e[8] = {y[nt][0].x, y[nt][0].y, y[nt][0].z, y[nt][0].w, y[nt][1].x, y[nt][1].y, y[nt][1].z, y[nt][1].w};
         uint32_t hi[4], lo[4];
-        split_fp8(e, down, hi, lo);
+        split_fp8(e, sc, hi, lo);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           q_hi[nt][0][j] = (int)hi[j];
@@ -514,7 +510,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(D, NT)) void k_kv_attn_few(
             const uint4 p0 = y[nt][4 * c + 2 * i], p1 = y[nt][4 * c + 2 * i + 1];
             const uint32_t e[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
             uint32_t hi[4], lo[4];
-            split_fp8(e, down, hi, lo);
+            split_fp8(e, sc, hi, lo);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               q_hi[nt][c][4 * i + j] = (int)hi[j];
@@ -846,7 +842,6 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
     for (int i = 0; i < 4 * KC; ++i) E = top_exponent(y[i], E);
     E = max(E, (uint32_t)__shfl_xor((int)E, 32));
     q_sc = query_scale(E);
-    const float down = __builtin_bit_cast(float, (254u - q_sc) << 23);
 #pragma unroll
     for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -854,7 +849,7 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
         const uint4 u = y[4 * c + 2 * i], v = y[4 * c + 2 * i + 1];
         const uint32_t e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
         uint32_t hi[4], lo[4];
-        split_fp8(e, down, hi, lo);
+        split_fp8(e, q_sc, hi, lo);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           q_hi[c][4 * i + j] = (int)hi[j];
@@ -1161,7 +1156,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvPar
 
 // ------------------------------------------------------------------------------- the launch
 
-constexpr int64_t kWorkers = 512, kManySegments = 1024, kWholeWorkers = 1 << 14, kLeastUnits = 12, kWholeTokens = 1280;
+constexpr int64_t kWorkers = 512, kManySegments = 1024, kLeastUnits = 12, kWholeTokens = 1280;
 constexpr int64_t kManySlots = 512, kLeastTokens = 512;
 
 // Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not
@@ -1174,6 +1169,8 @@ struct KvPlan {
   KvSplit many;
 };
 
+// Row tiles of the few-rows kernel, some of which may have no rows; a tile a request beside the other kernel.
+int64_t few_tiles(const KvAttnSizes& z, const KvPlan& p) { return p.rows_most == kAllRows ? row_tiles(z, p.R) : z.B; }
 size_t few_bytes(const KvAttnSizes& z, const KvPlan& p) {
   return p.rows_most > 0 && p.cut ? ((size_t)1 << p.lg) * (2 * p.R * (z.D + 2) * 4 + 16) : 0;
 }
@@ -1185,8 +1182,9 @@ KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   KvPlan p;
   const int64_t G = z.Hq / z.H, max_q = std::min(z.max_q, z.T), rows = max_q * G, few_rows = z.D == 256 ? 16 : 32;
   p.R = rows <= 16 || (rows > few_rows && G <= 16) || z.D == 256 ? 16 : 32;
-  if (rows <= few_rows) p.rows_most = kAllRows;
-  else if (z.T == z.B * max_q) p.rows_most = 0;  // every request has max_q rows
+  const bool fits = (z.T * G / p.R + z.B) * z.H <= (1 << 23);  // a launch holds under 2^32 threads
+  if (rows <= few_rows && fits) p.rows_most = kAllRows;
+  else if (z.T == z.B * max_q || rows <= few_rows) p.rows_most = 0;  // every request has max_q rows
   else p.rows_most = p.R;
   const int64_t longest = std::min(z.max_kv, (int64_t)1 << 30);
   // tokens that a tile of R rows sees at most
@@ -1197,11 +1195,8 @@ KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   const int64_t units = segments * ((span(p.R) + 31) / 32 + kSegmentUnits);
   p.cut = span(p.R) > kWholeTokens;
   const int64_t most = segments < kManySegments ? kWorkers : 2 * kWorkers;
-  const int64_t workers = p.cut ? std::min<int64_t>(most, units / kLeastUnits) : std::min<int64_t>(kWholeWorkers, segments);
-  for (p.lg = 0; ((int64_t)2 << p.lg) <= workers; ++p.lg) {
+  for (p.lg = 0; ((int64_t)2 << p.lg) <= std::min<int64_t>(most, units / kLeastUnits); ++p.lg) {
   }
-  if (!p.cut && ((int64_t)1 << p.lg) < workers) ++p.lg;
-
   p.parts = (int)(((int64_t)1 << p.lg) / std::max<int64_t>(segments, 1)) + 1;
   p.row_groups = (int)((std::min<int64_t>(rows, p.R) + 3) / 4);
 
@@ -1224,14 +1219,20 @@ hipError_t launch(const KvAttnArgs& a, const KvAttnSizes& z, const KvPlan& p, vo
   if (p.rows_most > 0) {
     const size_t slots = ((size_t)2 << p.lg) * p.R;
     KvShares sh = {p.lg, p.rows_most, nullptr, nullptr, nullptr};
+    constexpr int D2 = D == 256 ? 64 : D;  // R is 16 at D = 256
+    const dim3 block(kThreads);
     if (p.cut) {
       sh.o = static_cast<float*>(ws);
       sh.ml = reinterpret_cast<float2*>(sh.o + slots * D);
       sh.seams = reinterpret_cast<int4*>(sh.ml + slots);
+      const dim3 grid(1u << p.lg);
+      if (p.R == 16) hipLaunchKernelGGL((k_kv_attn_few<D, 1, true>), grid, block, 0, st, a, sh);
+      else hipLaunchKernelGGL((k_kv_attn_few<D2, 2, true>), grid, block, 0, st, a, sh);
+    } else {
+      const dim3 grid((unsigned)(few_tiles(z, p) * z.H));
+      if (p.R == 16) hipLaunchKernelGGL((k_kv_attn_few<D, 1, false>), grid, block, 0, st, a, sh);
+      else hipLaunchKernelGGL((k_kv_attn_few<D2, 2, false>), grid, block, 0, st, a, sh);
     }
-    const dim3 grid(1u << p.lg), block(kThreads);
-    if (p.R == 16) hipLaunchKernelGGL((k_kv_attn_few<D, 1>), grid, block, 0, st, a, sh);
-    else hipLaunchKernelGGL((k_kv_attn_few<D == 256 ? 64 : D, 2>), grid, block, 0, st, a, sh);  // R is 16 at D = 256
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (p.cut) {
@@ -1286,8 +1287,8 @@ void kv_attn_plan(const KvAttnSizes& z, size_t workspace_bytes, char* buf, size_
   const KvPlan p = plan_of(z, workspace_bytes);
   char few[96] = "", many[96] = "";
   if (p.rows_most > 0)
-    std::snprintf(few, sizeof few, "k_kv_attn_few<%d, %d> workers=%d%s", (int)z.D, p.R / 16, 1 << p.lg,
-                  p.cut ? " + k_kv_attn_seams" : "");
+    std::snprintf(few, sizeof few, p.cut ? "k_kv_attn_few<%d, %d, true> workers=%d + k_kv_attn_seams" : "k_kv_attn_few<%d, %d, false>",
+                  (int)z.D, p.R / 16, 1 << p.lg);
   if (p.rows_most < kAllRows)
     std::snprintf(many, sizeof many, "k_kv_attn_many<%d> C=%d S=%d%s", (int)z.D, p.many.C, p.many.S,
                   p.many.S > 1 ? " + k_kv_attn_join" : "");

@@ -92,24 +92,24 @@ def test_attention_argument_errors():
 def test_attention_plan_follows_rows_and_lengths():
     plan, ws = mx.mx_kv_attention_plan, mx.mx_kv_attention_workspace_bytes
     # decoding: equal shares of the tokens, more of them where there are many segments
-    assert plan(64, 64, 64, 8, 128, 1, 8192) == "k_kv_attn_few<128, 1> workers=512 + k_kv_attn_seams"
-    assert plan(512, 512, 64, 8, 128, 1, 2048) == "k_kv_attn_few<128, 1> workers=1024 + k_kv_attn_seams"
+    assert plan(64, 64, 64, 8, 128, 1, 8192) == "k_kv_attn_few<128, 1, true> workers=512 + k_kv_attn_seams"
+    assert plan(512, 512, 64, 8, 128, 1, 2048) == "k_kv_attn_few<128, 1, true> workers=1024 + k_kv_attn_seams"
     assert ws(64, 64, 64, 8, 128, 1, 8192) == 512 * (2 * 16 * (128 + 2) * 4 + 16)
     # short segments, also by a window, stay whole, one a worker and more
-    assert plan(32, 128, 12, 12, 64, 4, 4001, 1024) == "k_kv_attn_few<64, 1> workers=512"
-    assert plan(256, 256, 64, 8, 128, 1, 700) == "k_kv_attn_few<128, 1> workers=2048"
+    assert plan(32, 128, 12, 12, 64, 4, 4001, 1024) == "k_kv_attn_few<64, 1, false>"
+    assert plan(256, 256, 64, 8, 128, 1, 700) == "k_kv_attn_few<128, 1, false>"
     assert ws(256, 256, 64, 8, 128, 1, 700) == 0
     # up to 32 rows beside each other, 16 at D = 256
-    assert plan(4, 16, 32, 4, 128, 4, 100).startswith("k_kv_attn_few<128, 2>")
+    assert plan(4, 16, 32, 4, 128, 4, 100).startswith("k_kv_attn_few<128, 2, false>")
     assert plan(4, 16, 32, 4, 256, 4, 100) == "k_kv_attn_many<256> C=128 S=1"
     # whole prompts fill the chip; few tiles over a long cache are split
     assert plan(1, 8192, 32, 8, 128, 8192, 8192) == "k_kv_attn_many<128> C=8192 S=1"
     assert plan(1, 512, 32, 8, 128, 512, 16000) == "k_kv_attn_many<128> C=4032 S=4 + k_kv_attn_join"
     assert ws(1, 512, 32, 8, 128, 512, 16000) == 512 * 32 * (4 * 130 + 1) * 4
     # rows of both kinds: each kernel its own; without the workspace neither cuts
-    assert plan(20, 1553, 32, 4, 128, 512, 4096) == ("k_kv_attn_few<128, 1> workers=512 + k_kv_attn_seams + "
+    assert plan(20, 1553, 32, 4, 128, 512, 4096) == ("k_kv_attn_few<128, 1, true> workers=512 + k_kv_attn_seams + "
                                                      "k_kv_attn_many<128> C=4096 S=1")
-    assert plan(20, 1553, 32, 4, 128, 512, 4096, workspace_bytes=0) == ("k_kv_attn_few<128, 1> workers=512 + "
+    assert plan(20, 1553, 32, 4, 128, 512, 4096, workspace_bytes=0) == ("k_kv_attn_few<128, 1, false> + "
                                                                        "k_kv_attn_many<128> C=1073741824 S=1")
     for hint in (1, 10 ** 6, 2 ** 62):
         assert plan(3, 7, 8, 2, 64, hint, hint, 2 ** 62) != ""

@@ -57,13 +57,15 @@ __device__ __forceinline__ bool row_tile_of(const KvAttnArgs& a, int R, int b, i
   return true;
 }
 
-// Numbering row tiles without a sum over the requests: request b's tiles are
-// floor(cu_q[b] G / R) + b on, which leaves room for its ceil(n G / R) and never decreases. The
-// wave searches 64 requests at a time for the last one that starts at or before `tile`.
+// Numbering row tiles without a sum over the requests: tile b < B is request b's first; its others,
+// at most floor(n G / R), are the tiles B + floor(cu_q[b] G / R) on, for which the wave searches 64
+// requests at a time. Numbers without rows so come last: between the others they would leave some
+// XCDs without work (256 requests of 32 rows and 4 heads over up to 4000 tokens: 176 us so).
 __device__ __forceinline__ int first_tile(const KvAttnArgs& a, int R, int b) {
-  return (int)((int64_t)clamp_int(a.cu_q[b], 0, a.T) * a.G / R) + b;
+  return a.B + (int)((int64_t)clamp_int(a.cu_q[b], 0, a.T) * a.G / R);
 }
 __device__ __forceinline__ bool find_row_tile(const KvAttnArgs& a, int R, int tile, RowTile& w) {
+  if (tile < a.B) return row_tile_of(a, R, tile, 0, w);
   const int lane = threadIdx.x & 63;
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
@@ -73,8 +75,8 @@ __device__ __forceinline__ bool find_row_tile(const KvAttnArgs& a, int R, int ti
     hi = min(hi, lo + step);
   }
   lo = __builtin_amdgcn_readfirstlane(lo);
-  const int rb = tile - first_tile(a, R, lo);
-  return rb >= 0 && rb < (1 << 30) / R && row_tile_of(a, R, lo, rb * R, w);
+  const int i = tile - first_tile(a, R, lo) + 1;
+  return i > 0 && i < (1 << 30) / R && row_tile_of(a, R, lo, i * R, w);
 }
 int row_tiles(const KvAttnSizes& z, int R) { return (int)(z.T * (z.Hq / z.H) / R + z.B); }
 
@@ -269,14 +271,15 @@ constexpr int few_occupancy(int D, int NT) { return D == 64 ? (NT == 1 ? 4 : 3) 
 constexpr int kAllRows = 0x7FFFFFFF;
 
 // Work is cut into equal shares, however ragged the lengths are: a segment is a row tile and a
-// head, of ceil(tokens / 32) + kSegmentUnits units (a segment's start costs about as much as that
-// many units of 32 tokens); the segments of all requests lie in a row, and worker i of 2^lg takes
+// head, of ceil(tokens / 32) + kSegmentUnits units (a segment's start and end cost about as much as
+// that many units of 32 tokens: 64 requests x 8 heads x up to 8192 tokens 77, 74, 72, 72, 73 us at
+// 0, 4, 8, 16, 24); the segments of all requests lie in a row, and worker i of 2^lg takes
 // the units floor(i W / 2^lg) on of all W. A segment that lies in one share is written to the
 // output; of one that is cut, each worker leaves an unscaled part: in its slot 0 if the segment is
 // its first, else in its slot 1 (its last). The worker whose share begins in the second part of a
 // segment names the parts to the join.
 // Where every segment is short, or without a workspace, a workgroup takes one whole segment.
-constexpr int kSegmentUnits = 4;
+constexpr int kSegmentUnits = 8;
 
 struct KvShares {
   int lg;         // log2 of the workers
@@ -360,9 +363,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(D, NT)) void k_kv_attn_few(
     __syncthreads();
     b = __builtin_amdgcn_readfirstlane(found) * per;
     before = sums[__builtin_amdgcn_readfirstlane(found)];  // units before request b
-  } else if (sh.rows_most == kAllRows) {
-    if (!find_row_tile(a, R, worker / a.H, w)) return;
-  } else if (!row_tile_of(a, R, worker / a.H, 0, w) || w.n * a.G > sh.rows_most) {  // a tile a request
+  } else if (!find_row_tile(a, R, worker / a.H, w) || w.n * a.G > sh.rows_most) {
     return;
   }
 
@@ -1156,7 +1157,16 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvPar
 
 // ------------------------------------------------------------------------------- the launch
 
-constexpr int64_t kWorkers = 512, kManySegments = 1024, kLeastUnits = 12, kWholeTokens = 1280;
+// Workers that share the few-rows work: two a CU, twice that at D = 64 (whose registers let four run)
+// for kManySegments and more. 960 / 32 segments of D = 64: 91 / 22 us at 512 workers, 75 / 25 at 1024;
+// 128 x 8 heads x up to 8192 tokens at D = 128: 133 at 512, 152 at 1024. At least kLeastUnits units
+// each: 1 x 8 heads x 8192 tokens 15 us with 12, 19 with 4.
+constexpr int64_t kWorkers = 512, kManySegments = 256, kLeastUnits = 12;
+// Segments stay whole up to kWholeTokens tokens, or kWholeTimes of them for each segment there is (the
+// chip's workgroups then even out by their number). Whole / shared: 1 x 8 heads x 1200 tokens 12 / 14 us,
+// x 2400 18 / 15; 256 x 8 x up to 700 34 / 61; 64 x 8 x up to 2400 28 / 35; 128 x 8 x up to 4000 71 / 81,
+// up to 8192 159 / 133; 256 x 1 x up to 4000 40 / 28; 512 x 8 x up to 8192 499 / 537.
+constexpr int64_t kWholeTokens = 1280, kWholeTimes = 4;
 constexpr int64_t kManySlots = 512, kLeastTokens = 512;
 
 // Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not
@@ -1169,7 +1179,7 @@ struct KvPlan {
   KvSplit many;
 };
 
-// Row tiles of the few-rows kernel, some of which may have no rows; a tile a request beside the other kernel.
+// Row tiles of the few-rows kernel: beside the other kernel each request's first.
 int64_t few_tiles(const KvAttnSizes& z, const KvPlan& p) { return p.rows_most == kAllRows ? row_tiles(z, p.R) : z.B; }
 size_t few_bytes(const KvAttnSizes& z, const KvPlan& p) {
   return p.rows_most > 0 && p.cut ? ((size_t)1 << p.lg) * (2 * p.R * (z.D + 2) * 4 + 16) : 0;
@@ -1193,8 +1203,8 @@ KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   // few rows
   const int64_t segments = z.H * z.B * (p.rows_most == kAllRows ? (rows + p.R - 1) / p.R : 1);
   const int64_t units = segments * ((span(p.R) + 31) / 32 + kSegmentUnits);
-  p.cut = span(p.R) > kWholeTokens;
-  const int64_t most = segments < kManySegments ? kWorkers : 2 * kWorkers;
+  p.cut = span(p.R) > std::max(kWholeTokens, kWholeTimes * segments);
+  const int64_t most = z.D == 64 && segments >= kManySegments ? 2 * kWorkers : kWorkers;
   for (p.lg = 0; ((int64_t)2 << p.lg) <= std::min<int64_t>(most, units / kLeastUnits); ++p.lg) {
   }
   p.parts = (int)(((int64_t)1 << p.lg) / std::max<int64_t>(segments, 1)) + 1;
@@ -1236,9 +1246,10 @@ hipError_t launch(const KvAttnArgs& a, const KvAttnSizes& z, const KvPlan& p, vo
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (p.cut) {
-      // many parts: few segments, so of eight neighbouring workers one or two have a seam at most
+      // Many parts: four waves a row, and few segments, so of eight neighbouring workers one or two have a
+      // seam at most. Four waves / one: 65 parts 6.7 / 16 us, 33 parts 5.9 / 9.0, 17 parts 7.0 / 6.6, 9 parts 8.1 / 5.6.
       const unsigned workers = 1u << p.lg;
-      if (p.parts > 12)
+      if (p.parts > 24)
         hipLaunchKernelGGL((k_kv_attn_seams<D, 4>), dim3((workers + 7) / 8, p.row_groups), dim3(1024), 0, st, a, sh, p.R, 8);
       else
         hipLaunchKernelGGL((k_kv_attn_seams<D, 1>), dim3(workers, p.row_groups), dim3(256), 0, st, a, sh, p.R, 1);

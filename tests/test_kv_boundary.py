@@ -91,11 +91,14 @@ def test_attention_argument_errors():
 
 def test_attention_plan_follows_rows_and_lengths():
     plan, ws = mx.mx_kv_attention_plan, mx.mx_kv_attention_workspace_bytes
-    # decoding: equal shares of the tokens, more of them where there are many segments
+    # decoding: equal shares of the tokens, more of them where there are many segments of 64 elements
     assert plan(64, 64, 64, 8, 128, 1, 8192) == "k_kv_attn_few<128, 1, true> workers=512 + k_kv_attn_seams"
-    assert plan(512, 512, 64, 8, 128, 1, 2048) == "k_kv_attn_few<128, 1, true> workers=1024 + k_kv_attn_seams"
+    assert plan(512, 512, 64, 8, 128, 1, 20000) == "k_kv_attn_few<128, 1, true> workers=512 + k_kv_attn_seams"
+    assert plan(64, 64, 64, 8, 64, 1, 8192) == "k_kv_attn_few<64, 1, true> workers=1024 + k_kv_attn_seams"
+    assert plan(8, 8, 64, 8, 64, 1, 8192) == "k_kv_attn_few<64, 1, true> workers=512 + k_kv_attn_seams"
     assert ws(64, 64, 64, 8, 128, 1, 8192) == 512 * (2 * 16 * (128 + 2) * 4 + 16)
-    # short segments, also by a window, stay whole, one a worker and more
+    # short segments, also by a window, and very many of them, stay whole
+    assert plan(512, 512, 64, 8, 128, 1, 2048) == "k_kv_attn_few<128, 1, false>"
     assert plan(32, 128, 12, 12, 64, 4, 4001, 1024) == "k_kv_attn_few<64, 1, false>"
     assert plan(256, 256, 64, 8, 128, 1, 700) == "k_kv_attn_few<128, 1, false>"
     assert ws(256, 256, 64, 8, 128, 1, 700) == 0

@@ -20,7 +20,8 @@ namespace {
 constexpr int kScanThreads = 1024;
 constexpr int kOneGroupRequests = 1024;  // whose sums fit 12 KB of LDS
 // Rows that one workgroup fills by itself; past them the sums go through the workspace to a
-// second launch over the whole chip.
+// second launch over the whole chip. 96 requests, one launch / two: 96 rows 5.4 / 6.8 us, about 1600
+// 6.7 / 8.5, 4100 9.4 / 8.6, 6200 11.6 / 8.9; 1000 requests and 10000 rows 18.2 / 9.8.
 constexpr int kOneGroupRows = 4096;
 constexpr uint32_t kCap = (1u << 31) - 1;  // sums saturate here: larger than any valid one
 
@@ -201,70 +202,57 @@ __device__ __forceinline__ uint32_t quant8(const uint4& x, uint32_t s) {
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x.w), sc, 3);
 }
 
-// A workgroup quantizes 16 kPasses rows of 128 elements (two heads of 64, a head of 128 or half a
-// head of 256): a thread has 8 elements of a row at a time, four neighbours a block. K's codes go
-// out as they come, 16 bytes a block. V's lie four tokens to a word in the cache: its bytes meet in
-// LDS, and wherever four rows of the workgroup are the four tokens of a word, whatever row the
-// first of them is, whole words are written; other rows' bytes one by one.
-// Bound: HBM, 4 bytes read and 17/16 written per element of K and V.
-template <int kPasses>
+// A workgroup quantizes 16 rows of 128 elements (two heads of 64, a head of 128 or half a head of
+// 256): a thread has 8 elements of a row, four neighbours a block. K's codes go out as they come, 16
+// bytes a block. V's lie four tokens to a word in the cache: its bytes meet in LDS, and wherever four
+// rows of the workgroup are the four tokens of a word, whatever row the first of them is, whole words
+// are written; other rows' bytes one by one.
+// Bound: HBM, 4 bytes read and 17/16 written per element of K and V; at decoding sizes the launch.
+// 16411 rows x 8 x 128: 21.4 us (4.0 TB/s); 96 rows 3.7. With 64 rows a workgroup, fewer of whose
+// words are incomplete, 22.7 us (1024 rows 7.2 against 4.6): the L2 puts the words together as well.
+constexpr int kWriteRows = 16;
 __global__ __launch_bounds__(256) void k_kv_write(const uint16_t* __restrict__ k, int64_t k_stride,
                                                   const uint16_t* __restrict__ v, int64_t v_stride,
                                                   const int64_t* __restrict__ slots, int64_t T,
                                                   uint8_t* __restrict__ cache, int64_t num_slots, int lg, int heads,
                                                   int D) {
-  constexpr int kRows = 16 * kPasses;
-  __shared__ uint32_t v_words[kRows][17];  // a row's 16 words of codes (one more spreads rows over the banks)
-  __shared__ int64_t row_slot[kRows];      // -1: writes nothing
+  __shared__ uint32_t v_words[kWriteRows][17];  // a row's 16 words of codes (one more spreads rows over the banks)
+  __shared__ int64_t row_slot[kWriteRows];      // -1: writes nothing
   const KvLayout L = {1 << lg, D};
-  const int m = D / 32, c = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int e = (int)blockIdx.y * 128 + 8 * c, h = e / D, d = e % D;  // this thread's 8 elements of a row
-  const bool has = h < heads;
-  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < T; t0 += (int64_t)gridDim.x * kRows) {
-    uint4 kx[kPasses], vx[kPasses];
-    int64_t slot[kPasses];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int64_t t = t0 + 16 * i + group;
-      slot[i] = t < T ? slots[t] : -1;
-      if (slot[i] >= num_slots) slot[i] = -1;
-      kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
-      if (has && slot[i] >= 0) {
-        kx[i] = *reinterpret_cast<const uint4*>(k + t * k_stride + e);
-        vx[i] = *reinterpret_cast<const uint4*>(v + t * v_stride + e);
-      }
+  const int m = D / 32, c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int e = (int)blockIdx.y * 128 + 8 * c, h = e / D, d = e % D;  // this thread's 8 elements of row r
+  for (int64_t t0 = (int64_t)blockIdx.x * kWriteRows; t0 < T; t0 += (int64_t)gridDim.x * kWriteRows) {
+    const int64_t t = t0 + r;
+    int64_t slot = t < T ? slots[t] : -1;
+    if (slot >= num_slots) slot = -1;
+    const bool has = h < heads && slot >= 0;
+    const int tok = (int)(slot & (L.P - 1));
+    uint8_t* blk = cache + ((slot >> lg) * heads + h) * L.block_bytes();
+    uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
+    if (has) {
+      kx = *reinterpret_cast<const uint4*>(k + t * k_stride + e);
+      vx = *reinterpret_cast<const uint4*>(v + t * v_stride + e);
     }
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      uint32_t top = top_field(kx[i]) | top_field(vx[i]) << 16;  // both largest exponents
-      top = max_halves(top, (uint32_t)__shfl_xor((int)top, 1));
-      top = max_halves(top, (uint32_t)__shfl_xor((int)top, 2));
-      const uint32_t ek = top & 0xFFFFu, ev = top >> 16, sk = ek > 2u ? ek - 2u : 0u, sv = ev > 2u ? ev - 2u : 0u;
-      v_words[16 * i + group][c] = quant8(vx[i], sv);
-      if (c == 0) row_slot[16 * i + group] = slot[i];
-      if (has && slot[i] >= 0) {
-        const int tok = (int)(slot[i] & (L.P - 1));
-        uint8_t* blk = cache + ((slot[i] >> lg) * heads + h) * L.block_bytes();
-        *reinterpret_cast<uint32_t*>(blk + L.k_code(tok, d)) = quant8(kx[i], sk);
-        if ((c & 3) == 0) {
-          blk[L.k_scale(tok, d)] = (uint8_t)sk;
-          blk[L.v_scale(tok, d)] = (uint8_t)sv;
-        }
+    uint32_t top = top_field(kx) | top_field(vx) << 16;  // both largest exponents
+    top = max_halves(top, (uint32_t)__shfl_xor((int)top, 1));
+    top = max_halves(top, (uint32_t)__shfl_xor((int)top, 2));
+    const uint32_t ek = top & 0xFFFFu, ev = top >> 16, sk = ek > 2u ? ek - 2u : 0u, sv = ev > 2u ? ev - 2u : 0u;
+    v_words[r][c] = quant8(vx, sv);
+    if (c == 0) row_slot[r] = slot;
+    if (has) {
+      *reinterpret_cast<uint32_t*>(blk + L.k_code(tok, d)) = quant8(kx, sk);
+      if ((c & 3) == 0) {
+        blk[L.k_scale(tok, d)] = (uint8_t)sk;
+        blk[L.v_scale(tok, d)] = (uint8_t)sv;
       }
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {  // V's codes, row by row: the first of four tokens writes for all
-      const int r = kPasses * group + i;
-      const int64_t s = row_slot[r];
-      if (!has || s < 0) continue;
-      const int at = (int)(s & 3), first = r - at;
-      bool four = first >= 0 && first + 3 < kRows;
+    if (has) {  // V's codes: the first of four tokens writes for all
+      const int at = (int)(slot & 3), first = r - at;
+      bool four = first >= 0 && first + 3 < kWriteRows;
       if (four)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) four = four && row_slot[first + x] == s - at + x;
-      const int tok = (int)(s & (L.P - 1));
-      uint8_t* blk = cache + ((s >> lg) * heads + h) * L.block_bytes();
+        for (int x = 0; x < 4; ++x) four = four && row_slot[first + x] == slot - at + x;
       if (!four) {
         const uint32_t w = v_words[r][c];
 #pragma unroll
@@ -345,15 +333,10 @@ hipError_t launch_kv_write(const void* k, int64_t k_stride, const void* v, int64
                            int64_t T, void* cache, int64_t num_pages, int64_t P, int64_t heads, int64_t D,
                            hipStream_t st) {
   const int lg = __builtin_ctzll((unsigned long long)P);
-  // few rows: more workgroups of one pass; many: 64 rows, so that 60 or more of them are whole words' rows
-  const int rows = T <= 1024 ? 16 : 64;
-  const dim3 grid((unsigned)min((T + rows - 1) / rows, (int64_t)1 << 20), (unsigned)((heads * D + 127) / 128));
-  const auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, static_cast<const uint16_t*>(k), k_stride,
-                       static_cast<const uint16_t*>(v), v_stride, slots, T, static_cast<uint8_t*>(cache), num_pages * P, lg,
-                       (int)heads, (int)D);
-  };
-  if (rows == 16) launch(k_kv_write<1>); else launch(k_kv_write<4>);
+  const dim3 grid((unsigned)min((T + kWriteRows - 1) / kWriteRows, (int64_t)1 << 20), (unsigned)((heads * D + 127) / 128));
+  hipLaunchKernelGGL(k_kv_write, grid, dim3(256), 0, st, static_cast<const uint16_t*>(k), k_stride,
+                     static_cast<const uint16_t*>(v), v_stride, slots, T, static_cast<uint8_t*>(cache), num_pages * P, lg,
+                     (int)heads, (int)D);
   return hipGetLastError();
 }
 

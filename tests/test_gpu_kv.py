@@ -321,6 +321,23 @@ def test_attention_of_many_requests(B):
     c.check(mx, what="mixed")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_q,max_kv", [(1, 64), (1, 100000), (150, 400)])
+def test_attention_of_many_requests_of_several_tiles(D, max_q, max_kv):
+    """Row tiles past each request's first, searched for among more requests than a wave has lanes, in
+    each kernel: with a hint of one row the few-rows kernel takes them all, whole and shared."""
+    torch_or_skip()
+    mx = lib_or_fail()
+    rng = np.random.default_rng(D + max_q)
+    B = 131
+    kv = rng.integers(0, 120, B)
+    q = np.minimum(rng.integers(0, 3, B) * rng.integers(0, 20, B), 17)
+    kv[3], q[3] = 400, 150  # several tiles of 128 rows
+    kv[B - 1], q[B - 1] = 333, 90
+    c = Case(D, 2, 2, 16, q, kv, seed=B + D, extra_rows=5)
+    c.check(mx, max_q=max_q, max_kv=max_kv, what=f"hints {max_q} {max_kv}")
+
+
 # prompts and chunks: D, H, G, page, row counts, kv lengths
 MANY = [
     (64, 1, 1, 16, [33], [33]), (128, 1, 1, 16, [64, 65, 1], [64, 65, 100]), (256, 1, 1, 16, [40], [300]),

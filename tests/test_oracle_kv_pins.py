@@ -21,7 +21,7 @@ def test_layout_by_hand():
     assert KV.byte_of("k", 32, 128, 0, 1, 0) == 256 and KV.byte_of("k", 32, 128, 16, 0, 5) == 1029
     assert KV.byte_of("v", 32, 128, 0, 0, 0) == 2048 and KV.byte_of("v", 32, 128, 1, 0, 0) == 2049
     assert KV.byte_of("v", 32, 128, 0, 1, 0) == 2052 and KV.byte_of("v", 32, 128, 0, 0, 1) == 2064
-    assert KV.byte_of("v", 32, 128, 4, 0, 0) == 2048 + 256 and KV.byte_of("v", 32, 128, 16, 0, 0) == 3072
+    assert KV.byte_of("v", 32, 128, 4, 0, 0) == 2048 + 256 and KV.byte_of("v", 32, 128, 16, 0, 0) == 2048 + 1024
     assert KV.byte_of("ks", 32, 128, 3, 2) == 4096 + 35 and KV.byte_of("vs", 32, 128, 3, 2) == 4096 + 128 + 14
 
 

@@ -1178,6 +1178,13 @@ constexpr int64_t kWorkers = 512, kManySegments = 256, kLeastUnits = 12;
 // up to 8192 159 / 133; 256 x 1 x up to 4000 40 / 28; 512 x 8 x up to 8192 499 / 537.
 constexpr int64_t kWholeTokens = 1280, kWholeTimes = 4;
 constexpr int64_t kManySlots = 512, kLeastTokens = 512;
+// All requests in the few-rows kernel, in tiles of 32 rows (16 at D = 256, or where no request has more):
+// up to kFewRows rows each and kFewAverage on average. 64 requests x 4 heads x up to 4000 tokens, this way /
+// in the many-rows kernel: up to 16 rows 30 / 76 us, 32 39 / 79, 64 59 / 84, 128 74 / 110, but 128 rows each
+// 142 / 107; 32 rows at D = 256 65 / 157; 8 requests of up to 64 rows 29 / 25. Beside requests of more
+// rows the few-rows kernel takes those of one tile of 16 rows (32 where 16 heads are not enough for one):
+// 20 requests, most of one row, 14 us in tiles of 16, 17.5 in tiles of 32.
+constexpr int64_t kFewRows = 128, kFewAverage = 64;
 
 // Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not
 // launched), the others in the many-rows kernel (rows_most == kAllRows: not launched).
@@ -1200,11 +1207,11 @@ size_t many_bytes(const KvAttnSizes& z, const KvPlan& p) {
 
 KvPlan plan_of(const KvAttnSizes& z, size_t workspace_bytes) {
   KvPlan p;
-  const int64_t G = z.Hq / z.H, max_q = std::min(z.max_q, z.T), rows = max_q * G, few_rows = z.D == 256 ? 16 : 32;
-  p.R = rows <= 16 || (rows > few_rows && G <= 16) || z.D == 256 ? 16 : 32;
-  const bool fits = (z.T * G / p.R + z.B) * z.H <= (1 << 23);  // a launch holds under 2^32 threads
-  if (rows <= few_rows && fits) p.rows_most = kAllRows;
-  else if (z.T == z.B * max_q || rows <= few_rows) p.rows_most = 0;  // every request has max_q rows
+  const int64_t G = z.Hq / z.H, max_q = std::min(z.max_q, z.T), rows = max_q * G, all = std::min(z.T, z.B * max_q) * G;
+  const bool few = rows <= kFewRows && all <= kFewAverage * z.B;
+  p.R = rows <= 16 || (!few && G <= 16) || z.D == 256 ? 16 : 32;
+  if (few && (z.T * G / p.R + z.B) * z.H <= (1 << 23)) p.rows_most = kAllRows;  // a launch holds under 2^32 threads
+  else if (z.T == z.B * max_q || G > p.R) p.rows_most = 0;  // no request has so few rows
   else p.rows_most = p.R;
   const int64_t longest = std::min(z.max_kv, (int64_t)1 << 30);
   // tokens that a tile of R rows sees at most

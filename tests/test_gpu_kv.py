@@ -343,7 +343,8 @@ MANY = [
     (64, 1, 1, 16, [33], [33]), (128, 1, 1, 16, [64, 65, 1], [64, 65, 100]), (256, 1, 1, 16, [40], [300]),
     (128, 2, 4, 16, [17, 0, 130, 5], [17, 40, 500, 5]), (64, 2, 3, 64, [127, 128, 129], [127, 200, 513]),
     (128, 1, 8, 32, [300, 2], [301, 600]), (256, 2, 2, 128, [70, 150], [70, 151]), (128, 1, 16, 16, [40], [1030]),
-    (128, 1, 5, 16, [50, 3], [30, 2]), (64, 1, 40, 16, [1, 2], [100, 260]),
+    (128, 1, 5, 16, [50, 3], [30, 2]), (64, 1, 40, 16, [1, 2], [100, 260]), (64, 1, 1, 16, [133], [133]),
+    (128, 1, 1, 16, [129, 200, 1], [129, 200, 100]), (256, 1, 1, 16, [140], [300]), (64, 2, 40, 16, [3, 4, 5], [100, 260, 5]),
 ]
 
 
@@ -359,7 +360,8 @@ def test_attention_of_many_rows(D, H, G, page, q, kv):
 
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 63, 100, 1000, 2 ** 31 - 1, 2 ** 33])
 @pytest.mark.parametrize("D,q,kv", [(128, [1, 1, 4], [200, 17, 600]), (128, [70, 1, 33], [200, 1, 333]), (256, [40], [40]),
-                                    (64, [1, 90], [700, 128])])
+                                    (64, [1, 90], [700, 128]), (128, [170, 1, 33], [200, 1, 333]), (256, [140], [140]),
+                                    (64, [1, 190], [700, 228])])
 def test_attention_window(window, D, q, kv):
     torch_or_skip()
     mx = lib_or_fail()

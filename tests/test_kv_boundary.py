@@ -102,9 +102,14 @@ def test_attention_plan_follows_rows_and_lengths():
     assert plan(32, 128, 12, 12, 64, 4, 4001, 1024) == "k_kv_attn_few<64, 1, false>"
     assert plan(256, 256, 64, 8, 128, 1, 700) == "k_kv_attn_few<128, 1, false>"
     assert ws(256, 256, 64, 8, 128, 1, 700) == 0
-    # up to 32 rows beside each other, 16 at D = 256
+    # tiles of up to 32 rows, 16 at D = 256
     assert plan(4, 16, 32, 4, 128, 4, 100).startswith("k_kv_attn_few<128, 2, false>")
-    assert plan(4, 16, 32, 4, 256, 4, 100) == "k_kv_attn_many<256> C=128 S=1"
+    assert plan(4, 16, 32, 4, 256, 4, 100) == "k_kv_attn_few<256, 1, false>"
+    # more rows: by the longest request's and the average
+    assert plan(64, 512, 32, 4, 128, 8, 100) == "k_kv_attn_few<128, 2, false>"
+    assert plan(64, 1024, 32, 4, 128, 16, 100) == "k_kv_attn_many<128> C=128 S=1"
+    assert plan(64, 500, 32, 4, 128, 17, 100) == "k_kv_attn_few<128, 1, false> + k_kv_attn_many<128> C=128 S=1"
+    assert plan(64, 500, 80, 4, 256, 17, 100) == "k_kv_attn_many<256> C=128 S=1"
     # whole prompts fill the chip; few tiles over a long cache are split
     assert plan(1, 8192, 32, 8, 128, 8192, 8192) == "k_kv_attn_many<128> C=8192 S=1"
     assert plan(1, 512, 32, 8, 128, 512, 16000) == "k_kv_attn_many<128> C=4032 S=4 + k_kv_attn_join"

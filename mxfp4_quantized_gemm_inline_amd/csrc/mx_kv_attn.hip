@@ -29,7 +29,8 @@ constexpr float kLag = 8.f;
 struct RowTile {
   int b, q0, n, rb, rows;  // request, its first query row and count, first row of the tile, rows in it
   int len;                 // cached tokens
-  int lo, hi;              // tokens that some row of the tile sees (lo a multiple of 16; hi <= lo: none)
+  int seen, hi;            // tokens that some row of the tile sees (hi <= seen: none)
+  int lo;                  // seen, down to a multiple of 16: where its token tiles begin
   __device__ int pos(int r, int G) const { return len - n + r / G; }
 };
 
@@ -52,7 +53,8 @@ __device__ __forceinline__ bool row_tile_of(const KvAttnArgs& a, int R, int b, i
   w.rows = min(R, w.n * a.G - rb);
   if (w.rows <= 0) return false;
   w.len = (int)min((int64_t)max(a.kv_lens[b], 0), (int64_t)a.max_blocks << a.log2_page);
-  w.lo = row_begin(a, w.pos(rb, a.G)) & ~15;
+  w.seen = row_begin(a, w.pos(rb, a.G));
+  w.lo = w.seen & ~15;
   w.hi = row_end(a, w.len, w.pos(rb + w.rows - 1, a.G));
   return true;
 }
@@ -258,8 +260,9 @@ struct TokenTile {  // one lane's share of 16 tokens
   __device__ __forceinline__ float scale(uint32_t shift) const {
     return scale_at<(I * M + J) % 4>(vs[(I * M + J) / 4], shift);
   }
-  // Scales of the tokens outside [lo, hi) become 0 (2^-127): their codes, never written or
-  // written by another request, cannot be infinite then. t: the lane's first token.
+  // Scales of the tokens outside [lo, hi), which no row of the tile sees, become 0 (2^-127): bytes
+  // that were never written, or are another request's, could stand for infinities or NaN, which a
+  // weight of 0 does not take away. t: the lane's first token.
   __device__ __forceinline__ void mask(int t, int lo, int hi) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -398,7 +401,8 @@ __global__ __launch_bounds__(kThreads, few_occupancy(D, NT)) void k_kv_attn_few(
       w.len = __builtin_amdgcn_readfirstlane(req.len);
       w.rb = seg / a.H * R;
       w.rows = min(R, w.n * a.G - w.rb);
-      w.lo = row_begin(a, w.pos(w.rb, a.G)) & ~15;
+      w.seen = row_begin(a, w.pos(w.rb, a.G));
+      w.lo = w.seen & ~15;
       w.hi = row_end(a, w.len, w.pos(w.rb + w.rows - 1, a.G));
       const int to = (int)(min(u_end, seg_end) - seg_start), lo = w.lo;
       whole = from == 0 && to == units;
@@ -575,7 +579,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(D, NT)) void k_kv_attn_few(
           for (int i = 0; i < 2; ++i) {
             const int tt = t + 16 * i + 4 * g;
             const bool hidden = (bad2 >> i) & 1u;
-            x[i].mask(tt, w.lo, hidden ? 0 : w1);
+            x[i].mask(tt, w.seen, hidden ? 0 : w1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -938,7 +942,10 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
     v = global<words>(codes + (uint32_t)(P * (D / 2)) + (uint32_t)lane * (4u * M));
     vs = global<words>(codes + (lane_of((uint32_t)to_scales, tile) + P * M) + ((uint32_t)lane >> 4) * (4u * M));
   };
-  auto decode_v = [&](int step, int buf) {
+  // FIRST: of step 0, which alone can hold tokens before the first that is seen (with that comparison
+  // in the loop's decoding too: 6 x up to 1500 rows over up to 12001 tokens 280 us, so 273).
+  auto decode_v = [&](int step, int buf, auto FIRST) {
+    constexpr bool kFirst = FIRST;
     const int tile = 4 * step + wave, t = t0 + 16 * tile;
     TokenTile<D> x;
 #pragma unroll
@@ -947,7 +954,7 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
       x.vs[j] = vs[j];
     }
     const bool hidden = (hidden_tiles >> (tile - 32 * window)) & 1u;
-    if (t + 16 > t1 || hidden) x.mask(t + 4 * (lane >> 4), w.lo, hidden ? 0 : t1);
+    if ((kFirst && t < w.seen) || t + 16 > t1 || hidden) x.mask(t + 4 * (lane >> 4), kFirst ? w.seen : w.lo, hidden ? 0 : t1);
     uint2* dst = reinterpret_cast<uint2*>(&v_lds[buf][wave][0][((lane >> 4) & 1) * 32 + (lane & 15)]) + (lane >> 5);
     static_for<M>([&](auto J) {
       constexpr int j = J;
@@ -979,7 +986,7 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
     load_v(0);
     load_k(0, H0);
     load_k(0, H1);
-    decode_v(0, 0);
+    decode_v(0, 0, std::true_type{});
     load_v(1);
     scores(s0, H0);
     load_k(1, H0);
@@ -1060,11 +1067,11 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
       scores(s0, H0);
       weights(s1);
       load_k(st + 2, H0);
-      decode_v(st + 1, (st + 1) & 1);
+      decode_v(st + 1, (st + 1) & 1, std::false_type{});
       load_v(st + 2);
       values();
     } else {
-      decode_v(st + 1, (st + 1) & 1);
+      decode_v(st + 1, (st + 1) & 1, std::false_type{});
       load_v(st + 2);
     }
     __syncthreads();

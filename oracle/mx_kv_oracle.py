@@ -142,7 +142,6 @@ def attention(q, cache, table, cu_q, kv_lens, page, causal, window, scale):
     H = cache.shape[1]
     G = Hq // H
     out, bound = np.full((T, Hq, D), np.nan), np.full((T, Hq, D), np.nan)
-    u = 2.0 ** -24
     for b in range(len(kv_lens)):
         r0, r1, L = int(cu_q[b]), int(cu_q[b + 1]), int(kv_lens[b])
         n = r1 - r0
@@ -168,20 +167,26 @@ def attention(q, cache, table, cu_q, kv_lens, page, causal, window, scale):
             if not need.any():
                 out[r0:r1, hq] = bound[r0:r1, hq] = 0.0
                 continue
-            s = scale * (x @ k[:, h].T)
-            mag = scale * ((D + 8) * u * (np.abs(x) @ np.abs(k[:, h]).T)
-                           + 2.0 ** -21 * np.abs(x).max(axis=1, keepdims=True) * np.abs(k[:, h]).sum(axis=1)[None])
-            masked = np.where(seen, s, -np.inf)
-            top = masked.max(axis=1, keepdims=True)
-            some = np.isfinite(top)
-            w = np.exp(np.where(seen, s - np.where(some, top, 0.0), -np.inf))
-            tot = w.sum(axis=1, keepdims=True)
-            p = w / np.where(tot == 0, 1.0, tot)
-            eps = np.where(seen, mag + 6 * u * np.abs(s), 0.0).max(axis=1, keepdims=True)
-            eps = eps + 6 * u * np.where(seen, np.abs(s), 0.0).max(axis=1, keepdims=True)
-            o, A = p @ v[:, h], p @ np.abs(v[:, h])
-            rel = 2 * (2.0 ** -8 + 2 * eps + 2.0 ** -21) * 1.05 + 2 * (L + 16) * u
-            E = rel * A
-            out[r0:r1, hq] = o
-            bound[r0:r1, hq] = 2.0 ** -8 * np.abs(o) + (1 + 2.0 ** -8) * E + 1e-37
+            out[r0:r1, hq], bound[r0:r1, hq] = attend(x, k[:, h], v[:, h], seen, scale)
     return out, bound
+
+
+def attend(x, k, v, seen, scale):
+    """One head of one request: (out [n, D], bound [n, D]) of rows x [n, D] over k, v [L, D] with
+    seen [n, L]; the bound is the one that attention() derives."""
+    D, L = x.shape[1], k.shape[0]
+    u = 2.0 ** -24
+    s = scale * (x @ k.T)
+    mag = scale * ((D + 8) * u * (np.abs(x) @ np.abs(k).T)
+                   + 2.0 ** -21 * np.abs(x).max(axis=1, keepdims=True) * np.abs(k).sum(axis=1)[None])
+    masked = np.where(seen, s, -np.inf)
+    top = masked.max(axis=1, keepdims=True)
+    some = np.isfinite(top)
+    w = np.exp(np.where(seen, s - np.where(some, top, 0.0), -np.inf))
+    tot = w.sum(axis=1, keepdims=True)
+    p = w / np.where(tot == 0, 1.0, tot)
+    eps = np.where(seen, mag + 6 * u * np.abs(s), 0.0).max(axis=1, keepdims=True)
+    eps = eps + 6 * u * np.where(seen, np.abs(s), 0.0).max(axis=1, keepdims=True)
+    o, A = p @ v, p @ np.abs(v)
+    rel = 2 * (2.0 ** -8 + 2 * eps + 2.0 ** -21) * 1.05 + 2 * (L + 16) * u
+    return o, 2.0 ** -8 * np.abs(o) + (1 + 2.0 ** -8) * rel * A + 1e-37

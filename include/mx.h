@@ -391,12 +391,16 @@ mx_status mx_kv_read(const void* cache, int64_t num_pages, int64_t page_size, in
  *    mx_kv_attention_workspace_bytes(...) bytes; always optional: with a NULL or smaller one
  *    the tokens are split less or not at all. Calls that may overlap need one each; nothing in
  *    it needs clearing.
- * Queries are not quantized (a row is used exactly down to 2^-21 of its largest element);
- * scores and the softmax's maximum and sum are FP32; the weights are rounded to bf16 for the
- * product with V, whose sum is FP32; the result is rounded once. Output is bitwise reproducible
- * for the same arguments. Requires 0 <= T <= 2^30 / heads_q, heads_q <= 1024, 0 <= B <= 2^22 /
- * heads (and 2^20), 1 <= max_blocks, max_blocks * page_size <= 2^30, scale finite and > 0,
- * |scale * q . K| below 1e38 and the cache's sizes as above. T == 0 or B == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE,
+ * Queries are not quantized: elements down to 2^-13 of their row's largest are used exactly,
+ * smaller ones to within 2^-21 of it. Scores and the softmax's maximum and sum are FP32; the
+ * weights are rounded to bf16 for the product with V, whose sum is FP32; the result is rounded
+ * once. Output is bitwise reproducible for the same arguments.
+ * The sums have to stay in FP32's range, for each row over the tokens it sees: the sum over d of
+ * |q_d K_d|, and scale times it, below 1e38; each element's sum of |V| over the tokens below
+ * 2^120 (the weights reach 2^8 before the division).
+ * Requires 0 <= T <= 2^30 / heads_q, heads_q <= 1024, 0 <= B <= 2^22 / heads (and 2^20),
+ * 1 <= max_blocks, max_blocks * page_size <= 2^30, 0 < scale <= 2^127 and the cache's sizes as
+ * above. T == 0 or B == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE,
  * MX_ERR_ALIGN (q, out, cache, workspace: 16 bytes; tables: 4), MX_ERR_DEVICE, MX_ERR_HIP.
  */
 mx_status mx_kv_attention(const void* q_bf16, int64_t q_stride, const void* cache, int64_t num_pages,

@@ -1,7 +1,5 @@
 // mx_kv_api.cpp - the C ABI of the paged MXFP4 key/value cache: argument validation (pure host
 // code, before any HIP call), the gfx950 check and dispatch to the launchers.
-#include <cmath>
-
 #include "mx.h"
 #include "mx_internal.h"
 #include "mx_kv.h"
@@ -14,6 +12,7 @@ constexpr int64_t kMaxStride = int64_t(1) << 32;  // elements: rows times stride
 constexpr int64_t kMaxPages = int64_t(1) << 31;
 constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxTiles = int64_t(1) << 22;   // requests times heads: a launch holds under 2^32 threads
+constexpr float kMaxScale = 0x1p127f;             // times log2 e it is finite in FP32
 constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of one request: positions stay in 32 bits, also past a tile's end
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -112,7 +111,7 @@ mx_status mx_kv_attention(const void* q_bf16, int64_t q_stride, const void* cach
   const mx::KvAttnSizes z = {B, T, heads_q, heads, D, max_q, max_kv, window};
   if (!attn_sizes_ok(z) || mx_kv_cache_bytes(num_pages, page_size, heads, D) == 0 ||
       !table_ok(max_blocks, page_size) || (causal != 0 && causal != 1) || (window > 0 && !causal) ||
-      !std::isfinite(scale) || scale <= 0.f || !stride_ok(q_stride, 0) || !stride_ok(out_stride, heads_q * D))
+      !(scale > 0.f && scale <= kMaxScale) || !stride_ok(q_stride, 0) || !stride_ok(out_stride, heads_q * D))
     return MX_ERR_SHAPE;
   if (T == 0 || B == 0) return MX_OK;
   if (!q_bf16 || !cache || !block_table || !cu_q || !kv_lens || !out_bf16) return MX_ERR_NULL;

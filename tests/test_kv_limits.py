@@ -1,0 +1,26 @@
+"""Calls of the key/value cache that the library refuses on the host, and what its host functions
+answer for unusual arguments. None of these runs anything on a GPU."""
+import os
+
+import pytest
+
+import mxfp4_quantized_gemm_inline_amd as mx
+
+pytestmark = pytest.mark.skipif(not os.path.exists(mx.LIB_PATH), reason="libmxgemm.so not built")
+
+
+def attention_status(**changes):
+    args = dict(q=0x10000, qs=1024, cache=0x20000, pages=9, page=16, table=0x30000, blocks=4, cu=0x40000, kv=0x50000, B=2, T=5,
+                Hq=8, H=2, D=128, max_q=3, max_kv=60, causal=1, window=0, scale=0.1, out=0x60000, os=1024, ws=None, ws_bytes=0,
+                stream=None)
+    args.update(changes)
+    return mx.lib().mx_kv_attention(*args.values())
+
+
+def test_attention_scale_ends():
+    """The kernels multiply scores by scale * log2 e, which has to be finite in FP32. T == 0 shows that
+    a scale inside the range passes the check without a launch."""
+    for scale in (2.0 ** -149, 2.0 ** -126, 1.0, 2.0 ** 127):
+        assert attention_status(scale=scale, T=0) == mx.MX_OK, scale
+    for scale in (2.0 ** 127 * (1 + 2.0 ** -23), 2.5e38, 3.4e38, float("inf"), float("nan"), 0.0, -0.5):
+        assert attention_status(scale=scale, T=0) == mx.MX_ERR_SHAPE, scale

@@ -520,8 +520,13 @@ def _pointers(names, *tensors):
 
 
 @functools.lru_cache(maxsize=1024)
+def _kv_workspace_bytes(call: str, *sizes: int) -> int:
+    """The library's answer by the sizes' values (ints only: another number's hash may be its identity)."""
+    return int(getattr(lib(), call)(*sizes))
+
+
 def mx_kv_tables_workspace_bytes(B: int, max_rows: int) -> int:
-    return int(lib().mx_kv_tables_workspace_bytes(int(B), int(max_rows)))
+    return _kv_workspace_bytes("mx_kv_tables_workspace_bytes", int(B), int(max_rows))
 
 
 def mx_kv_tables(old_lens, new_lens, block_table, free_pages, free_count, page_size: int, max_rows: int, cu_q=None,
@@ -610,11 +615,10 @@ def mx_kv_read(cache, slots, heads: int, D: int, page_size: int, k_out=None, v_o
     return k, v
 
 
-@functools.lru_cache(maxsize=1024)
 def mx_kv_attention_workspace_bytes(B: int, T: int, heads_q: int, heads: int, D: int, max_q: int, max_kv: int,
                                     window: int = 0) -> int:
-    return int(lib().mx_kv_attention_workspace_bytes(int(B), int(T), int(heads_q), int(heads), int(D), int(max_q),
-                                                     int(max_kv), int(window)))
+    return _kv_workspace_bytes("mx_kv_attention_workspace_bytes", int(B), int(T), int(heads_q), int(heads), int(D), int(max_q),
+                               int(max_kv), int(window))
 
 
 def mx_kv_attention(q_bf16, cache, block_table, cu_q, kv_lens, heads: int, page_size: int, causal: bool = True,

@@ -24,3 +24,17 @@ def test_attention_scale_ends():
         assert attention_status(scale=scale, T=0) == mx.MX_OK, scale
     for scale in (2.0 ** 127 * (1 + 2.0 ** -23), 2.5e38, 3.4e38, float("inf"), float("nan"), 0.0, -0.5):
         assert attention_status(scale=scale, T=0) == mx.MX_ERR_SHAPE, scale
+
+
+def test_workspace_sizes_follow_their_arguments_values():
+    """Whole numbers in any type that int() takes, also one whose value changes between two calls."""
+    torch = pytest.importorskip("torch")
+    n = torch.tensor(5000)
+    assert mx.mx_kv_tables_workspace_bytes(n, 100) == mx.mx_kv_tables_workspace_bytes(5000, 100) > 0
+    n.fill_(4)
+    assert mx.mx_kv_tables_workspace_bytes(n, 100) == 0
+    n.fill_(8192)
+    long = mx.mx_kv_attention_workspace_bytes(64, 64, 64, 8, 128, 1, n)
+    assert long == mx.mx_kv_attention_workspace_bytes(64, 64, 64, 8, 128, 1, 8192) > 0
+    n.fill_(100)
+    assert mx.mx_kv_attention_workspace_bytes(64, 64, 64, 8, 128, 1, n) == 0

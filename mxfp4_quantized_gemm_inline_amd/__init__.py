@@ -485,6 +485,12 @@ def _meta(t, name, dtype, least=0):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _workspace_size(t):
+    """Bytes of a workspace, a contiguous tensor of any type."""
+    _meta(t, "workspace", getattr(t, "dtype", None))
+    return t.numel() * t.element_size()
+
+
 def _rows3(t, name):
     """(rows, heads, D, row stride) of a bf16 [rows, heads, D] tensor whose rows are dense (a
     slice of columns of a wider row-major tensor is)."""
@@ -565,8 +571,7 @@ def mx_kv_tables(old_lens, new_lens, block_table, free_pages, free_count, page_s
     nbytes, ws_bytes = mx_kv_tables_workspace_bytes(B, max_rows), 0
     if nbytes:
         workspace = workspace if workspace is not None else _new((nbytes,), torch.uint8, block_table, stream)
-        _meta(workspace, "workspace", workspace.dtype)
-        ws_bytes = workspace.numel() * workspace.element_size()
+        ws_bytes = _workspace_size(workspace)
     else:
         workspace = None
     old_, new_, table_, stack_, count_, out_, cu_, slots_, pos_, status_, ws_ = _pointers(
@@ -660,8 +665,7 @@ def mx_kv_attention(q_bf16, cache, block_table, cu_q, kv_lens, heads: int, page_
         workspace = None
     ws_bytes = 0
     if workspace is not None:
-        _meta(workspace, "workspace", workspace.dtype)
-        ws_bytes = workspace.numel() * workspace.element_size()
+        ws_bytes = _workspace_size(workspace)
     q_, cache_, table_, cu_, kv_, out_, ws_ = _pointers(
         "q_bf16 cache block_table cu_q kv_lens out workspace", q_bf16, cache, block_table, cu_q, kv_lens, out, workspace)
     _check(lib().mx_kv_attention(q_, q_stride, cache_, pages, page_size, table_, max_blocks, cu_, kv_, B, T, heads_q, heads,

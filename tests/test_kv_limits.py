@@ -38,3 +38,18 @@ def test_workspace_sizes_follow_their_arguments_values():
     assert long == mx.mx_kv_attention_workspace_bytes(64, 64, 64, 8, 128, 1, 8192) > 0
     n.fill_(100)
     assert mx.mx_kv_attention_workspace_bytes(64, 64, 64, 8, 128, 1, n) == 0
+
+
+def test_a_workspace_that_is_no_tensor_is_a_type_error():
+    torch = pytest.importorskip("torch")
+    i32 = torch.int32
+    q = torch.zeros((5, 4, 64), dtype=torch.bfloat16)
+    cache = torch.zeros(mx.mx_kv_cache_bytes(2, 16, 2, 64), dtype=torch.uint8)
+    table, lens, cu = torch.zeros((3, 4), dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(4, dtype=i32)
+    for bad in (4096, "none", True):
+        with pytest.raises(TypeError):
+            mx.mx_kv_attention(q, cache, table, cu, lens, 2, 16, workspace=bad)
+        with pytest.raises(TypeError):
+            mx.mx_kv_tables(lens, lens, table, torch.zeros(6, dtype=i32), torch.zeros(1, dtype=i32), 16, 1 << 20, workspace=bad)
+    with pytest.raises(ValueError):
+        mx.mx_kv_attention(q, cache, table, cu, lens, 2, 16, workspace=torch.zeros((8, 64))[:, ::2])

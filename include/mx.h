@@ -385,8 +385,8 @@ mx_status mx_kv_read(const void* cache, int64_t num_pages, int64_t page_size, in
  *    entry outside [0, num_pages) makes its tokens unseen.
  *  cu_q: [B+1] int32, non-decreasing from 0 (clamped to [0, T]); kv_lens: [B] int32 (clamped
  *    to [0, max_blocks * page_size]).
- *  max_q, max_kv: the most rows and the longest kv_len of any request: they size the launch
- *    and nothing else (any value >= 1 is correct).
+ *  max_q, max_kv: the most rows and the longest kv_len of any request: hints that choose the
+ *    kernels, their cuts and the workspace, right at any value >= 1.
  *  workspace: partial results where the tokens of a request are split over the chip, of
  *    mx_kv_attention_workspace_bytes(...) bytes; always optional: with a NULL or smaller one
  *    the tokens are split less or not at all. Calls that may overlap need one each; nothing in
@@ -394,7 +394,9 @@ mx_status mx_kv_read(const void* cache, int64_t num_pages, int64_t page_size, in
  * Queries are not quantized: elements down to 2^-13 of their row's largest are used exactly,
  * smaller ones to within 2^-21 of it. Scores and the softmax's maximum and sum are FP32; the
  * weights are rounded to bf16 for the product with V, whose sum is FP32; the result is rounded
- * once. Output is bitwise reproducible for the same arguments.
+ * once. Output is bitwise reproducible for the same arguments; which kernels run, and so the last
+ * bits, go by all sizes and hints. A head of a row whose elements are not all finite is unspecified
+ * itself and changes no other.
  * The sums have to stay in FP32's range, for each row over the tokens it sees: the sum over d of
  * |q_d K_d|, and scale times it, below 1e38; each element's sum of |V| over the tokens below
  * 2^120 (the weights reach 2^8 before the division).

@@ -5,8 +5,8 @@ import pytest
 
 from oracle import mx_kv_oracle as KV
 
-from gpu_util import lib_or_fail, torch_or_skip
-from test_gpu_kv import Case
+from gpu_util import dev_bf16, host_bits, lib_or_fail, torch_or_skip
+from test_gpu_kv import Case, _close
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,62 @@ def test_tokens_before_every_window_need_no_bytes(D, H, G, page, q, kv, window, 
     plan = plan_of(mx, c, window, workspace=workspace)
     assert all(k in plan for k in kernels), plan
     c.check(mx, window=window, workspace=workspace, what=plan)
+
+
+# D, H, G, page, q, kv, what the plan names: lengths that end inside pages and token tiles
+ENDS = [
+    (64, 2, 3, 64, [1, 4], [201, 90], ["k_kv_attn_few<64, 1, false>"]),
+    (64, 1, 8, 64, [4, 4], [201, 90], ["k_kv_attn_few<64, 2, false>"]),
+    (128, 2, 3, 64, [1, 4], [201, 90], ["k_kv_attn_few<128, 1, false>"]),
+    (128, 1, 8, 64, [4, 4], [3001, 1700], ["k_kv_attn_few<128, 2, true>"]),
+    (256, 1, 2, 64, [1, 3], [201, 90], ["k_kv_attn_few<256, 1, false>"]),
+    (256, 1, 2, 64, [1, 1], [3001, 1700], ["k_kv_attn_few<256, 1, true>"]),
+    (64, 1, 1, 64, [140, 1], [3001, 90], ["k_kv_attn_many<64>", "k_kv_attn_join"]),
+    (128, 1, 1, 64, [140, 150], [201, 150], ["k_kv_attn_many<128>"]),
+    (256, 1, 1, 64, [140, 1], [201, 90], ["k_kv_attn_many<256>"]),
+]
+
+
+@pytest.mark.parametrize("D,H,G,page,q,kv,kernels", ENDS)
+def test_bytes_past_the_ends_change_no_bit(D, H, G, page, q, kv, kernels):
+    """Whatever codes and scales stand behind a request's last token in its last page, and in pages
+    that no table names, the result is the same bit for bit."""
+    torch_or_skip()
+    mx = lib_or_fail()
+    c = Case(D, H, G, page, q, kv, seed=D + sum(q))
+    plan = plan_of(mx, c)
+    assert all(k in plan for k in kernels), plan
+    first = c.check(mx, what=plan)
+    rng = np.random.default_rng(1)
+    used = {int(p) for row, L in zip(c.table, kv) for p in row[:-(-L // page)]}
+    for scales in (lambda *n: rng.integers(0, 256, n), lambda *n: np.full(n, 255), lambda *n: np.full(n, 254), lambda *n: np.zeros(n)):
+        for b, L in enumerate(kv):
+            fill_tokens(c, b, range(L, -(-L // page) * page), lambda *n: rng.integers(0, 256, n), scales)
+        for p in set(range(c.pages)) - used:
+            c.cache[p] = rng.integers(0, 256, c.cache[p].shape)
+        assert np.array_equal(first, c.check(mx, what=plan))
+
+
+@pytest.mark.parametrize("D,q,kv", [(64, [1, 3], [90, 201]), (128, [1, 3], [90, 201]), (256, [1, 3], [90, 201]),
+                                    (128, [1, 1], [3001, 90]), (64, [140, 3], [201, 90]), (128, [140, 3], [1600, 90]),
+                                    (256, [140, 3], [201, 90])])
+@pytest.mark.parametrize("value", [0x7FC0, 0x7F80, 0xFF80])
+def test_queries_that_are_not_finite_stay_in_their_row(D, q, kv, value):
+    """NaN and infinities in one head of one row of each request: every other row and head is right."""
+    torch_or_skip()
+    mx = lib_or_fail()
+    c = Case(D, 2, 2, 16, q, kv, seed=D, extra_rows=3)
+    exact, bound = c.exact()
+    n = int(c.cu[-1])
+    fine = np.ones(exact.shape[:2], dtype=bool)
+    fine[n:] = False
+    for b in range(len(q)):
+        row, head = int(c.cu[b]) + q[b] // 2, 1 + b
+        c.q[row, head, 5 + 31 * b] = value
+        fine[row, head] = False
+    c.q[n:] = value  # rows of no request
+    import torch
+    out = torch.full((c.T, 4, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    mx.mx_kv_attention(dev_bf16(c.q), *c.args(), out=out, max_q=max(q), max_kv=max(kv))
+    _close(host_bits(out)[fine], exact[fine], bound[fine], plan_of(mx, c))
+    assert bool((out[n:] == 7).all())

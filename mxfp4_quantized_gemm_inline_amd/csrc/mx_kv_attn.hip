@@ -5,7 +5,7 @@
 // in one pass over the tokens: with the running maximum m, sum l and unscaled output o, a
 // block of tokens with maximum m' multiplies l and o by exp(m - max(m, m')) and adds its own.
 #include <algorithm>
-#include <cmath>
+#include <climits>
 #include <cstdio>
 
 #include "mx_device.h"
@@ -942,8 +942,8 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
     v = global<words>(codes + (uint32_t)(P * (D / 2)) + (uint32_t)lane * (4u * M));
     vs = global<words>(codes + (lane_of((uint32_t)to_scales, tile) + P * M) + ((uint32_t)lane >> 4) * (4u * M));
   };
-  // FIRST: of step 0, which alone can hold tokens before the first that is seen (with that comparison
-  // in the loop's decoding too: 6 x up to 1500 rows over up to 12001 tokens 280 us, so 273).
+  // FIRST: of step 0, which alone can hold tokens before the first that is seen (with that bound in
+  // the loop's decoding too: 6 x up to 1500 rows over up to 12001 tokens 280 us, so 271).
   auto decode_v = [&](int step, int buf, auto FIRST) {
     constexpr bool kFirst = FIRST;
     const int tile = 4 * step + wave, t = t0 + 16 * tile;
@@ -954,7 +954,7 @@ __global__ __launch_bounds__(64 * kManyWaves, D == 256 ? 1 : 2) void k_kv_attn_m
       x.vs[j] = vs[j];
     }
     const bool hidden = (hidden_tiles >> (tile - 32 * window)) & 1u;
-    if ((kFirst && t < w.seen) || t + 16 > t1 || hidden) x.mask(t + 4 * (lane >> 4), kFirst ? w.seen : w.lo, hidden ? 0 : t1);
+    if ((kFirst && t < w.seen) || t + 16 > t1 || hidden) x.mask(t + 4 * (lane >> 4), kFirst ? w.seen : INT_MIN, hidden ? 0 : t1);
     uint2* dst = reinterpret_cast<uint2*>(&v_lds[buf][wave][0][((lane >> 4) & 1) * 32 + (lane & 15)]) + (lane >> 5);
     static_for<M>([&](auto J) {
       constexpr int j = J;

@@ -634,9 +634,11 @@ def mx_kv_attention(q_bf16, cache, block_table, cu_q, kv_lens, heads: int, page_
     token. Returns out [T, heads_q, D] bf16.
 
     scale defaults to D ** -0.5. max_q and max_kv (the most rows and the longest length of any
-    request; hints only) default to T and to the table's width. workspace: a device tensor for
-    partial results, None to allocate mx_kv_attention_workspace_bytes(...) bytes through torch,
-    or False to pass none.
+    request) choose the kernels and their cuts and change no result but its last bits. They default
+    to T and to the table's width, for which a batch pays: 64 single rows over up to 8192 tokens take
+    144 us and 43 MB of workspace without max_q, 75 us and 8.5 MB with max_q=1. workspace: a device
+    tensor for partial results, None to allocate mx_kv_attention_workspace_bytes(...) bytes through
+    torch, or False to pass none.
     """
     torch = _torch()
     i32 = torch.int32

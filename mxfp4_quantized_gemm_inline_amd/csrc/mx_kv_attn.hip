@@ -17,8 +17,9 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.0e38f;  // the running maximum before any token: below every score
 // How far, in powers of two, the maximum in use may lag behind the true one before the sums are
-// rescaled: weights reach 2^8 then, which neither bf16's relative rounding nor an FP32 sum feels,
-// and the rescaling of all sums is left out of nearly every step.
+// rescaled (a published step of attention kernels): weights reach 2^8 then, which neither bf16's
+// relative rounding nor an FP32 sum feels, and the rescaling of all sums is left out of nearly every
+// step.
 constexpr float kLag = 8.f;
 
 // ------------------------------------------------------------------------------- row tiles
@@ -275,7 +276,8 @@ struct TokenTile {  // one lane's share of 16 tokens
   }
 };
 
-// Waves a SIMD that the registers allow without spilling.
+// Waves a SIMD that the vector registers allow without spilling (the shared kernels keep 66 to 72 scalars
+// of their schedule in lanes of one).
 constexpr int few_occupancy(int D, int NT) { return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 3 : 2) : 2; }
 
 constexpr int kAllRows = 0x7FFFFFFF;
@@ -1180,17 +1182,23 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a, int S, KvPar
 // each: 1 x 8 heads x 8192 tokens 15 us with 12, 19 with 4.
 constexpr int64_t kWorkers = 512, kManySegments = 256, kLeastUnits = 12;
 // Segments stay whole up to kWholeTokens tokens, or kWholeTimes of them for each segment there is (the
-// chip's workgroups then even out by their number). Whole / shared: 1 x 8 heads x 1200 tokens 12 / 14 us,
-// x 2400 18 / 15; 256 x 8 x up to 700 34 / 61; 64 x 8 x up to 2400 28 / 35; 128 x 8 x up to 4000 71 / 81,
-// up to 8192 159 / 133; 256 x 1 x up to 4000 40 / 28; 512 x 8 x up to 8192 499 / 537.
+// chip's workgroups then even out by their number). Whole / shared at D = 128, lengths from an eighth to
+// all of so many tokens. The rule keeps whole: 1 x 8 heads x 1200 12.8 / 14.4 us, 8 x 8 x 1200 14.5 / 17.3,
+// 64 x 8 x 2000 25.5 / 31.2, 128 x 8 x 4000 79 / 84, 256 x 8 x 700 37 / 53, 256 x 8 x 4000 145 / 145. It
+// shares: 1 x 8 x 1500 14.2 / 13.4, 1 x 8 x 2400 19.4 / 14.6, 8 x 8 x 2400 23.9 / 18.1, 64 x 8 x 4000 49 / 48,
+// x 8192 90 / 74, 128 x 8 x 8192 149 / 141, 256 x 1 x 4000 36.5 / 29.5. Near the border it can take the slower
+// side: 64 x 8 x 2400 33.9 / 36.7 (shared; 51.5 / 58.2 at D = 256, 22.1 / 29.5 at 64), 256 x 1 x 2000
+// 22.2 / 24.6 (shared), 256 x 8 x 8192 277 / 254 and 512 x 8 x 8192 494 / 476 (whole).
 constexpr int64_t kWholeTokens = 1280, kWholeTimes = 4;
 constexpr int64_t kManySlots = 512, kLeastTokens = 512;
 // All requests in the few-rows kernel, in tiles of 32 rows (16 at D = 256, or where no request has more):
-// up to kFewRows rows each and kFewAverage on average. 64 requests x 4 heads x up to 4000 tokens, this way /
-// in the many-rows kernel: up to 16 rows 30 / 76 us, 32 39 / 79, 64 59 / 84, 128 74 / 110, but 128 rows each
-// 142 / 107; 32 rows at D = 256 65 / 157; 8 requests of up to 64 rows 29 / 25. Beside requests of more
-// rows the few-rows kernel takes those of one tile of 16 rows (32 where 16 heads are not enough for one):
-// 20 requests, most of one row, 14 us in tiles of 16, 17.5 in tiles of 32.
+// up to kFewRows rows each and kFewAverage on average. Otherwise requests of more rows than a tile go to the
+// many-rows kernel. This way / otherwise, 4 heads over up to 4000 tokens, rows from an eighth to all of so
+// many: 64 requests of 16 rows 30 / 49 us, 32 38 / 87, 64 53 / 95; 8 requests of 16 rows 19.6 / 24.4, 64
+// 29.5 / 54; 1 of 64 rows 17.4 / 24.1; 16 of 128 rows, 63 on average, 33 / 69, 4 of 128, 64, 30 / 31; at
+// D = 256 64 of 32 rows 62 / 160, 8 of 64 31 / 66. But 64 requests of 128 rows each 142 this way, 107
+// otherwise. Beside requests of more rows the few-rows kernel takes those of one tile of 16 rows (32 where
+// 16 heads are not enough for one): 20 requests, most of one row, 14 us in tiles of 16, 17.5 in tiles of 32.
 constexpr int64_t kFewRows = 128, kFewAverage = 64;
 
 // Which kernels run: requests of at most rows_most rows in the few-rows kernel (0: it is not

@@ -53,3 +53,13 @@ def test_a_workspace_that_is_no_tensor_is_a_type_error():
             mx.mx_kv_tables(lens, lens, table, torch.zeros(6, dtype=i32), torch.zeros(1, dtype=i32), 16, 1 << 20, workspace=bad)
     with pytest.raises(ValueError):
         mx.mx_kv_attention(q, cache, table, cu, lens, 2, 16, workspace=torch.zeros((8, 64))[:, ::2])
+
+
+def test_attention_plan_without_the_hint_of_rows():
+    """max_q defaults to T: right for one request, further launches and workspace for a batch of rows."""
+    plan, ws = mx.mx_kv_attention_plan, mx.mx_kv_attention_workspace_bytes
+    assert plan(64, 64, 64, 8, 128, 64, 8192) == ("k_kv_attn_few<128, 1, true> workers=512 + k_kv_attn_seams + "
+                                                  "k_kv_attn_many<128> C=512 S=16 + k_kv_attn_join")
+    assert ws(64, 64, 64, 8, 128, 64, 8192) == ws(64, 64, 64, 8, 128, 1, 8192) + 64 * 64 * (16 * 130 + 1) * 4
+    # one request: 8 heads of 2400 rows in tiles of 128 are 150 groups, three times which fit the chip
+    assert plan(1, 300, 64, 8, 128, 300, 8192) == "k_kv_attn_many<128> C=2752 S=3 + k_kv_attn_join"

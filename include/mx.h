@@ -290,6 +290,61 @@ mx_status mx_a4w4_gemm_grouped_mx_plan(int64_t N, int64_t K, int64_t rows_hint, 
                                        size_t buf_len);
 
 /* ------------------------------------------------------------------------------------------
+ * Routing to experts, and the tables that the grouped GEMMs and the combine take: what stands
+ * between a router's logits and mx_a4w4_gemm_grouped / mx_moe_combine.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Score of an expert's logit, and the type of the logits. */
+enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SIGMOID = 1 };
+enum { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 };
+
+/*
+ * The topk experts of each token and their weights. With l = logits[t]:
+ *   s[e] = softmax(l)[e] or 1 / (1 + exp(-l[e]));   c[e] = s[e] + bias[e]  (s[e] where bias is NULL);
+ *   groups > 1: the experts stand in `groups` groups of E / groups neighbours; a group's value is the
+ *     sum of its group_top (1 or 2) largest c, and only the topk_groups best groups stay;
+ *   topk_ids[t]: the topk experts with the largest c of those, largest first;
+ *   topk_weights[t][i] = scale * s[id], with renormalize != 0 over the sum of s over the chosen (0
+ *     where that sum is 0).
+ * Equal c go to the lower expert, equal values to the lower group. c and values are FP64 and are
+ * compared to 42 bits (without a bias c is compared by the logits, exactly); weights are formed in
+ * FP64 and rounded once. An expert whose logit or bias is -inf or NaN is never chosen and has no part
+ * in any sum; +inf counts as FP32's largest number. Where fewer than topk experts are left, the rest
+ * of the places get id -1 and weight 0, which mx_moe_sort and mx_moe_combine pass over.
+ *  logits: row t's E values of logits_type at element t * logits_stride (any address of that type).
+ *  bias: [E] float32, or NULL. num_rows: [1] int32 or NULL: rows from *num_rows on are padding, all
+ *  of their places get id -1 and weight 0. topk_ids: [T, topk] int32, topk_weights: [T, topk] float32.
+ * Requires 0 <= T <= 2^30 / topk, 1 <= E <= 1024, 1 <= topk <= min(64, topk_groups * E / groups),
+ * 1 <= groups <= 64, E % groups == 0, 1 <= topk_groups <= groups, 0 <= logits_stride < 2^32, a finite
+ * scale. T == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (logits: their type's
+ * size; the others 4 bytes), MX_ERR_DEVICE, MX_ERR_HIP.
+ */
+mx_status mx_moe_route(const void* logits, int64_t logits_stride, int32_t logits_type, const float* bias,
+                       int64_t T, int64_t E, int64_t topk, int32_t score, int64_t groups, int64_t topk_groups,
+                       int32_t group_top, int32_t renormalize, float scale, const int32_t* num_rows,
+                       int32_t* topk_ids, float* topk_weights, hipStream_t stream);
+
+/*
+ * The chosen experts sorted: the tables of mx_a4w4_gemm_grouped and mx_moe_combine for the E experts
+ * first_expert .. first_expert + E - 1 (all of them, or one device's share). The places of topk_ids
+ * [T, topk] whose id is among these are ordered by expert, those of one expert by token and place;
+ * R is their number.
+ *  expert_offsets: [E + 1] int32, where each expert's rows start; expert_offsets[E] = R.
+ *  row_token: [T * topk] int32, the token of each row; -1 from row R on.
+ *  token_rows: [T, topk] int32, the row of each place; -1 where the id is none of these experts'.
+ * workspace: mx_moe_sort_workspace_bytes(T, topk, E) bytes (0 for few places: NULL), 16-byte aligned.
+ * Requires T >= 0, 1 <= topk <= 1024, T * topk <= 2^28, 1 <= E <= 1024, 0 <= first_expert < 2^30. The
+ * outputs may not overlap topk_ids. Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (4 bytes;
+ * workspace 16), MX_ERR_WORKSPACE, MX_ERR_DEVICE, MX_ERR_HIP.
+ */
+mx_status mx_moe_sort(const int32_t* topk_ids, int64_t T, int64_t topk, int64_t first_expert, int64_t E,
+                      int32_t* expert_offsets, int32_t* row_token, int32_t* token_rows, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace mx_moe_sort needs. 0 for sizes it refuses. */
+size_t mx_moe_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E);
+
+/* ------------------------------------------------------------------------------------------
  * A key/value cache in MXFP4, in pages, and the attention that reads it: what a decoder
  * layer runs between the GEMM that makes its queries, keys and values and the one that takes
  * the attention's output. Keys and values are quantized row by row with the rule at the top
@@ -424,6 +479,77 @@ size_t mx_kv_attention_workspace_bytes(int64_t B, int64_t T, int64_t heads_q, in
 mx_status mx_kv_attention_plan(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t D, int64_t max_q,
                                int64_t max_kv, int64_t window, size_t workspace_bytes, char* buf,
                                size_t buf_len);
+
+/* How mx_kv_append pairs the elements that it rotates: i with i + rot / 2, or 2 i with 2 i + 1. */
+enum { MX_ROPE_HALVES = 0, MX_ROPE_PAIRS = 1 };
+
+/*
+ * What stands between the projection to queries, keys and values and mx_kv_attention, in one pass:
+ * norms of each head, rotation by position, and the keys and values into the cache. For every head x
+ * [D] of row t's queries and keys:
+ *   y = x * weight / sqrt(mean(x^2) + eps)      (y = x where weight is NULL);
+ *   element pairs (a, b) of the first `rot` elements, number i of rot / 2 of them, become
+ *   (a cos - b sin, a sin + b cos) with the angle positions[t] * inv_freq[i], formed in FP64, and cos
+ *   and sin times rope_scale.
+ * Queries are worked out in FP32 and rounded once to bf16, to q_out. Keys are worked out in FP64 and
+ * rounded to FP32, values are taken as they are, and both are quantized with the rule at the top of
+ * this file into slot slots[t] of the cache, as mx_kv_write does.
+ *  q_bf16, k_bf16, v_bf16: row t's heads_q * D (heads * D) values at element t * q_stride (k_stride,
+ *    v_stride); q_out likewise with q_out_stride >= heads_q * D. Strides are multiples of 8. q_out may
+ *    be q_bf16 itself (with the same stride) and must not overlap any input otherwise.
+ *  Without queries, q_bf16 NULL and heads_q 0; without keys and values (a layer that reads another's
+ *    cache), k_bf16, v_bf16, slots and cache NULL, heads and num_pages 0.
+ *  positions: [T] int32; a row whose position is below 0 is padding: nothing of it is read or written.
+ *  slots: [T] int64; a slot outside [0, num_pages * page_size) writes no key and value (its queries
+ *    are still done). Give each slot once.
+ *  q_weight, k_weight: [D] float32 or NULL. inv_freq: [rot / 2] float32; NULL with rot 0 for none.
+ * Requires 0 <= T <= 2^30, heads and heads_q at most 1024, one of them above 0, D 64, 128 or 256,
+ * rot a multiple of 16 in [0, D], eps >= 0 and finite, a finite rope_scale, page_size as above (also
+ * without keys). Elements, weights and frequencies must be finite, and so must keys after norm and
+ * rotation in FP32. T == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (q, k, v,
+ * q_out, cache: 16 bytes; slots: 8; the others 4), MX_ERR_DEVICE, MX_ERR_HIP.
+ */
+mx_status mx_kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,
+                       const void* v_bf16, int64_t v_stride, const int32_t* positions, const int64_t* slots,
+                       int64_t T, int64_t heads_q, int64_t heads, int64_t D, void* cache, int64_t num_pages,
+                       int64_t page_size, const float* q_weight, const float* k_weight, float eps,
+                       const float* inv_freq, int64_t rot, int32_t rope, float rope_scale, void* q_out,
+                       int64_t q_out_stride, hipStream_t stream);
+
+/*
+ * Verification of drafted tokens against the target model's probabilities, and the next token, from
+ * random numbers that the caller gives; the lengths it returns are mx_kv_tables' new_lens for the
+ * following step (drafts taken back). Request b's rows are cu_q[b] .. cu_q[b+1] - 1, as for
+ * mx_kv_attention: first its last token, then its drafts, so that tokens[r + 1] is what row r's
+ * distribution p = target_probs[r] judges. From its first row on, with q = draft_probs[r], the draft
+ * x = tokens[r + 1] is accepted while
+ *   accept_random[r] * q[x] < p[x]     (q[x] = 1 where draft_probs is NULL: drafts without chance)
+ * and, at the first row that refuses, the next token is drawn from max(p - q, 0) (p without x where
+ * draft_probs is NULL; p itself where that is 0 everywhere); after the last draft it is drawn from p.
+ * Drawn from w: the least j with w[0] + .. + w[j] > u * (sum of w), u = sample_random[b] in [0, 1). All
+ * of this is FP64. Probabilities below 0 and NaN count as 0, and rows need not sum to 1; u below 0 or
+ * NaN counts as 0 and above 1 as 1 (the last token with a weight); an accept_random that is NaN and a
+ * draft outside [0, V) refuse.
+ *  target_probs, draft_probs: row r's V float32 at element r * target_stride (r * draft_stride).
+ *  tokens: [T] int32. cu_q: [B + 1] int32, non-decreasing from 0 (clamped to [0, T]). kv_lens: [B]
+ *    int32, with this step's rows. accept_random: [T], sample_random: [B] float32.
+ *  out_tokens: [T] int32: at a request's rows its accepted drafts, then the drawn token (-1 where p is
+ *    0 everywhere), then -1; -1 from row cu_q[B] on.
+ *  accepted: [B] int32, how many drafts. new_lens: [B] int32, kv_lens[b] less the refused drafts (kv_lens
+ *    itself may be given).
+ *  A request without rows has 0 accepted and keeps its length.
+ * workspace: mx_verify_drafts_workspace_bytes(B, V) bytes, 16-byte aligned. Requires 0 <= T <= 2^30,
+ * 0 <= B <= 2^16 - 2, 1 <= V <= 2^24, strides in [V, 2^32) (or 0). Errors: MX_ERR_NULL, MX_ERR_SHAPE,
+ * MX_ERR_ALIGN (4 bytes; workspace 16), MX_ERR_WORKSPACE, MX_ERR_DEVICE, MX_ERR_HIP.
+ */
+mx_status mx_verify_drafts(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                           int64_t draft_stride, const int32_t* tokens, const int32_t* cu_q,
+                           const int32_t* kv_lens, const float* accept_random, const float* sample_random,
+                           int64_t T, int64_t B, int64_t V, int32_t* out_tokens, int32_t* accepted,
+                           int32_t* new_lens, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace mx_verify_drafts needs. 0 for sizes it refuses, and for B == 0. */
+size_t mx_verify_drafts_workspace_bytes(int64_t B, int64_t V);
 
 #ifdef __cplusplus
 }

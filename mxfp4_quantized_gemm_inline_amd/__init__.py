@@ -54,6 +54,15 @@ SIGNATURES = {
                                  _vp]),
     "mx_kv_attention_workspace_bytes": (_c_sz, [_c_i64] * 8),
     "mx_kv_attention_plan": (_c_int, [_c_i64] * 8 + [_c_sz, ctypes.c_char_p, _c_sz]),
+    "mx_moe_route": (_c_int, [_vp, _c_i64, _c_int, _vp, _c_i64, _c_i64, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_int,
+                              ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "mx_moe_sort": (_c_int, [_vp, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _c_sz, _vp]),
+    "mx_moe_sort_workspace_bytes": (_c_sz, [_c_i64] * 3),
+    "mx_kv_append": (_c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _c_i64,
+                              _c_i64, _vp, _vp, ctypes.c_float, _vp, _c_i64, _c_int, ctypes.c_float, _vp, _c_i64, _vp]),
+    "mx_verify_drafts": (_c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp,
+                                  _vp, _c_sz, _vp]),
+    "mx_verify_drafts_workspace_bytes": (_c_sz, [_c_i64] * 2),
     "mx_calib_read": (_c_int, [_vp, _c_sz, _c_i64, _vp, _vp]),
     "mx_calib_mfma": (_c_int, [_c_i64, _c_i64, _vp, _vp]),
     "mx_calib_mfma_flops": (ctypes.c_double, [_c_i64, _c_i64]),
@@ -64,6 +73,8 @@ SIGNATURES = {
 
 MX_OK, MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_DEVICE, MX_ERR_WORKSPACE, MX_ERR_HIP = range(7)
 MX_ACT_SILU, MX_ACT_SWIGLU = 0, 1
+MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID = 0, 1
+MX_ROPE_HALVES, MX_ROPE_PAIRS = 0, 1
 
 _lib = None
 
@@ -688,6 +699,205 @@ def mx_kv_attention_plan(B: int, T: int, heads_q: int, heads: int, D: int, max_q
     return buf.value.decode()
 
 
+def mx_kv_append(q_bf16, k_bf16, v_bf16, positions, slots, cache, page_size: int, inv_freq=None, rope: int = MX_ROPE_HALVES,
+                 rope_scale: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, stream=None):
+    """Queries [T, heads_q, D], keys and values [T, heads, D] (bf16, rows dense, any row stride) on their
+    way from a projection to mx_kv_attention: each head of queries and keys normed (q_weight, k_weight
+    float32 [D], or None), its first 2 * len(inv_freq) elements rotated by positions (int32 [T]; below 0:
+    padding, skipped) times inv_freq (float32, or None), keys and values quantized into the cache's slots
+    (int64 [T]). Returns the queries, bf16 [T, heads_q, D] (q_out, which may be q_bf16 itself).
+
+    q_bf16 may be None (no queries); k_bf16, v_bf16, slots and cache may be None together (a layer that
+    reads another's cache)."""
+    torch = _torch()
+    f32 = torch.float32
+    T = heads_q = heads = q_stride = k_stride = v_stride = out_stride = pages = 0
+    if q_bf16 is not None:
+        T, heads_q, D, q_stride = _rows3(q_bf16, "q_bf16")
+    elif q_out is not None:
+        raise ValueError("q_out without q_bf16")
+    if k_bf16 is not None:
+        Tk, heads, Dk, k_stride = _rows3(k_bf16, "k_bf16")
+        if q_bf16 is not None and (Tk, Dk) != (T, D):
+            raise ValueError(f"k_bf16 must have shape {(T, heads, D)}, got {tuple(k_bf16.shape)}")
+        T, D = Tk, Dk
+        *v_shape, v_stride = _rows3(v_bf16, "v_bf16")
+        if tuple(v_shape) != (T, heads, D):
+            raise ValueError(f"v_bf16 must have shape {(T, heads, D)}, got {tuple(v_shape)}")
+        _meta(slots, "slots", torch.int64, T)
+        pages = _kv_pages(cache, page_size, heads, D)
+    elif q_bf16 is None:
+        raise ValueError("neither queries nor keys")
+    elif v_bf16 is not None or slots is not None or cache is not None:
+        raise ValueError("k_bf16, v_bf16, slots and cache go together")
+    _meta(positions, "positions", torch.int32, T)
+    if q_weight is not None:
+        _meta(q_weight, "q_weight", f32, D)
+    if k_weight is not None:
+        _meta(k_weight, "k_weight", f32, D)
+    rot = 0
+    if inv_freq is not None:
+        _meta(inv_freq, "inv_freq", f32)
+        rot = 2 * inv_freq.numel()
+    if q_bf16 is not None:
+        if q_out is None:
+            q_out, out_stride = _new((T, heads_q, D), torch.bfloat16, q_bf16, stream), heads_q * D
+        else:
+            *shape, out_stride = _rows3(q_out, "q_out")
+            if tuple(shape) != (T, heads_q, D):
+                raise ValueError(f"q_out must have shape {(T, heads_q, D)}, got {tuple(shape)}")
+    if T == 0:
+        return q_out
+    pos_, q_, k_, v_, slots_, cache_, qw_, kw_, freq_, out_ = _pointers(
+        "positions q_bf16 k_bf16 v_bf16 slots cache q_weight k_weight inv_freq q_out", positions, q_bf16, k_bf16, v_bf16, slots, cache,
+        q_weight, k_weight, inv_freq, q_out)
+    _check(lib().mx_kv_append(q_, q_stride, k_, k_stride, v_, v_stride, pos_, slots_, T, heads_q, heads, D, cache_, pages,
+                              int(page_size), qw_, kw_, float(eps), freq_, rot, int(rope), float(rope_scale), out_, out_stride,
+                              _stream_ptr(stream)), "mx_kv_append")
+    return q_out
+
+
+def mx_verify_drafts_workspace_bytes(B: int, V: int) -> int:
+    return _kv_workspace_bytes("mx_verify_drafts_workspace_bytes", int(B), int(V))
+
+
+def mx_verify_drafts(target_probs, draft_probs, tokens, cu_q, kv_lens, accept_random, sample_random, out_tokens=None, accepted=None,
+                     new_lens=None, workspace=None, stream=None):
+    """Drafts against the target's probabilities: request b's rows cu_q[b] .. cu_q[b+1] - 1 of tokens (int32
+    [T]) are its last token and its drafts, target_probs and draft_probs (float32 [T, V]; draft_probs None
+    for drafts without chance) the distributions after each row, accept_random [T] and sample_random [B]
+    (float32) the numbers in [0, 1) that decide. Returns (out_tokens int32 [T]: accepted drafts, then the
+    next token, then -1; accepted int32 [B]; new_lens int32 [B]: kv_lens less the refused drafts)."""
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    T, V, p_stride = _rows2(target_probs, "target_probs", (f32,))
+    q_stride = 0
+    if draft_probs is not None:
+        Tq, Vq, q_stride = _rows2(draft_probs, "draft_probs", (f32,))
+        if (Tq, Vq) != (T, V):
+            raise ValueError(f"draft_probs must have shape {(T, V)}, got {(Tq, Vq)}")
+    _meta(tokens, "tokens", i32, T)
+    _meta(kv_lens, "kv_lens", i32)
+    B = kv_lens.numel()
+    _meta(cu_q, "cu_q", i32, B + 1)
+    _meta(accept_random, "accept_random", f32, T)
+    _meta(sample_random, "sample_random", f32, B)
+    if out_tokens is None and accepted is None and new_lens is None:
+        out_tokens, accepted, new_lens = _new((T + 2 * B,), i32, target_probs, stream).split((T, B, B))
+    else:
+        out_tokens = out_tokens if out_tokens is not None else _new((T,), i32, target_probs, stream)
+        accepted = accepted if accepted is not None else _new((B,), i32, target_probs, stream)
+        new_lens = new_lens if new_lens is not None else _new((B,), i32, target_probs, stream)
+        _meta(out_tokens, "out_tokens", i32, T)
+        _meta(accepted, "accepted", i32, B)
+        _meta(new_lens, "new_lens", i32, B)
+    nbytes, ws_bytes = mx_verify_drafts_workspace_bytes(B, V), 0
+    if nbytes:
+        workspace = workspace if workspace is not None else _new((nbytes,), torch.uint8, target_probs, stream)
+        ws_bytes = _workspace_size(workspace)
+    else:
+        workspace = None
+    p_, q_, tokens_, cu_, kv_, accept_, sample_, out_, acc_, lens_, ws_ = _pointers(
+        "target_probs draft_probs tokens cu_q kv_lens accept_random sample_random out_tokens accepted new_lens workspace",
+        target_probs, draft_probs, tokens, cu_q, kv_lens, accept_random, sample_random, out_tokens, accepted, new_lens, workspace)
+    _check(lib().mx_verify_drafts(p_, p_stride, q_, q_stride, tokens_, cu_, kv_, accept_, sample_, T, B, V, out_, acc_, lens_, ws_,
+                                  ws_bytes, _stream_ptr(stream)), "mx_verify_drafts")
+    return out_tokens, accepted, new_lens
+
+
+# ----------------------------------------------------------------------------- routing to experts
+
+def _rows2(t, name, dtype):
+    """(rows, columns, row stride) of a 2-D tensor whose rows are dense."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtype:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtype)}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    (T, N), (row, one) = t.shape, t.stride()
+    if N > 1 and one != 1:
+        raise ValueError(f"{name} must have dense rows, got strides {t.stride()}")
+    return T, N, row if T > 1 else N
+
+
+def mx_moe_route(logits, topk: int, bias=None, score: int = MX_SCORE_SOFTMAX, groups: int = 1, topk_groups: int = 1,
+                 group_top: int = 2, renormalize: bool = True, scale: float = 1.0, num_rows=None, ids=None, weights=None,
+                 stream=None):
+    """The topk experts of each token and their weights, (ids int32, weights float32) [T, topk], from a
+    router's logits [T, E] (bf16 or float32, rows dense, any row stride).
+
+    Experts are chosen by softmax or sigmoid score plus bias (float32 [E]), largest first, ties to the
+    lower expert; with groups > 1 only among the topk_groups groups whose group_top best sum highest.
+    Weights are the scores without the bias, over their sum where renormalize, times scale. Rows from
+    num_rows (int32 [1], on the device) on are padding: id -1, weight 0, as for places that too few
+    unmasked experts leave over."""
+    torch = _torch()
+    T, E, stride = _rows2(logits, "logits", (torch.bfloat16, torch.float32))
+    topk = int(topk)
+    shape = (T, max(topk, 0))
+    if bias is not None:
+        _meta(bias, "bias", torch.float32, E)
+    if num_rows is not None:
+        _meta(num_rows, "num_rows", torch.int32, 1)
+    if ids is None:
+        ids = _new(shape, torch.int32, logits, stream)
+    elif _meta(ids, "ids", torch.int32) or ids.shape != shape:
+        raise ValueError(f"ids must have shape {shape}, got {tuple(ids.shape)}")
+    if weights is None:
+        weights = _new(shape, torch.float32, logits, stream)
+    elif _meta(weights, "weights", torch.float32) or weights.shape != shape:
+        raise ValueError(f"weights must have shape {shape}, got {tuple(weights.shape)}")
+    logits_, bias_, rows_, ids_, weights_ = _pointers("logits bias num_rows ids weights", logits, bias, num_rows, ids, weights)
+    _check(lib().mx_moe_route(logits_, stride, 1 if logits.dtype is torch.float32 else 0, bias_, T, E, topk, int(score), int(groups),
+                              int(topk_groups), int(group_top), 1 if renormalize else 0, float(scale), rows_, ids_, weights_,
+                              _stream_ptr(stream)), "mx_moe_route")
+    return ids, weights
+
+
+def mx_moe_sort_workspace_bytes(T: int, topk: int, E: int) -> int:
+    return _kv_workspace_bytes("mx_moe_sort_workspace_bytes", int(T), int(topk), int(E))
+
+
+def mx_moe_sort(topk_ids, E: int, first_expert: int = 0, expert_offsets=None, row_token=None, token_rows=None, workspace=None,
+                stream=None):
+    """The tables of the grouped GEMMs and the combine for the E experts from first_expert on, from
+    topk_ids (int32 [T, topk], contiguous; ids of other experts have no row): (expert_offsets int32
+    [E + 1], row_token int32 [T * topk], token_rows int32 [T, topk])."""
+    torch = _torch()
+    i32 = torch.int32
+    _meta(topk_ids, "topk_ids", i32)
+    T, topk = _dims2(topk_ids, "topk_ids")
+    E = int(E)
+    if expert_offsets is None and row_token is None and token_rows is None:
+        # one allocation; each part starts at a multiple of 16 bytes
+        n, m = T * topk, max(E, 0) + 1
+        n4, m4 = (n + 3) // 4 * 4, (m + 3) // 4 * 4
+        whole = _new((m4 + 2 * n4,), i32, topk_ids, stream)
+        expert_offsets, row_token, token_rows = whole[:m], whole[m4:m4 + n], whole[m4 + n4:m4 + n4 + n].view(T, topk)
+    else:
+        expert_offsets = expert_offsets if expert_offsets is not None else _new((max(E, 0) + 1,), i32, topk_ids, stream)
+        row_token = row_token if row_token is not None else _new((T * topk,), i32, topk_ids, stream)
+        token_rows = token_rows if token_rows is not None else _new((T, topk), i32, topk_ids, stream)
+        _meta(expert_offsets, "expert_offsets", i32, E + 1)
+        _meta(row_token, "row_token", i32, T * topk)
+        _meta(token_rows, "token_rows", i32)
+        if token_rows.shape != (T, topk):
+            raise ValueError(f"token_rows must have shape {(T, topk)}, got {tuple(token_rows.shape)}")
+    nbytes, ws_bytes = mx_moe_sort_workspace_bytes(T, topk, E), 0
+    if nbytes:
+        workspace = workspace if workspace is not None else _new((nbytes,), torch.uint8, topk_ids, stream)
+        ws_bytes = _workspace_size(workspace)
+    else:
+        workspace = None
+    ids_, offsets_, token_, rows_, ws_ = _pointers("topk_ids expert_offsets row_token token_rows workspace", topk_ids, expert_offsets,
+                                                   row_token, token_rows, workspace)
+    _check(lib().mx_moe_sort(ids_, T, topk, int(first_expert), E, offsets_, token_, rows_, ws_, ws_bytes, _stream_ptr(stream)),
+           "mx_moe_sort")
+    return expert_offsets, row_token, token_rows
+
+
 def mx_calib_read(buf, ctas: int, sink, stream=None) -> None:
     """One streaming-read launch over the whole of `buf` (a contiguous device tensor whose
     byte size is a multiple of 16); `sink` is a device tensor of at least 4 bytes."""
@@ -749,7 +959,9 @@ __all__ = [
     "mx_a4w4_gemm_plan", "mx_a16w4_gemm_plan", "mx_a4w4_gemm_grouped_plan", "mx_a4w4_gemm_grouped_act_quant",
     "mx_a4w4_gemm_grouped_act_quant_plan", "mx_a4w4_gemm_grouped_mx", "mx_a4w4_gemm_grouped_mx_plan",
     "mx_moe_combine", "mx_a16w4_gemm", "mx_kv_cache_bytes", "mx_kv_tables", "mx_kv_tables_workspace_bytes",
-    "mx_kv_write", "mx_kv_read", "mx_kv_attention", "mx_kv_attention_workspace_bytes", "mx_kv_attention_plan", "MX_ACT_SILU", "MX_ACT_SWIGLU", "mx_calib_read", "mx_calib_mfma",
+    "mx_kv_write", "mx_kv_read", "mx_kv_attention", "mx_kv_attention_workspace_bytes", "mx_kv_attention_plan", "mx_kv_append",
+    "mx_verify_drafts", "mx_verify_drafts_workspace_bytes", "mx_moe_route", "mx_moe_sort", "mx_moe_sort_workspace_bytes",
+    "MX_SCORE_SOFTMAX", "MX_SCORE_SIGMOID", "MX_ROPE_HALVES", "MX_ROPE_PAIRS", "MX_ACT_SILU", "MX_ACT_SWIGLU", "mx_calib_read", "mx_calib_mfma",
     "mx_calib_mfma_flops", "mx_calib_mfma_operands", "mx_calib_mfma_operands_flops",
     "mx_calib_mfma_operands_clock",
 ]

@@ -108,6 +108,28 @@ __device__ __forceinline__ uint32_t quant_block(const uint32_t (&x)[16], uint32_
   return s;
 }
 
+// ---- a block held by four lanes, 8 elements each
+
+// The largest bf16 exponent field of 8 elements.
+__device__ __forceinline__ uint32_t top_field(const uint4& u) {
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[i] & 0x7F807F80u));
+  return (uint32_t)(m.x > m.y ? m.x : m.y) >> 7;
+}
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+// 8 elements' codes at a block's scale byte: as quant_block, a scale byte of 0 is passed as 2^-127.
+__device__ __forceinline__ uint32_t quant8(const uint4& x, uint32_t s) {
+  const float sc = __builtin_bit_cast(float, s ? s << 23 : 0x00400000u);
+  uint32_t r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0, __builtin_bit_cast(bf16x2, x.x), sc, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x.y), sc, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x.z), sc, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x.w), sc, 3);
+}
+
 // Load one 32-element bf16 block (64 bytes, 16-byte aligned) into 16 words.
 __device__ __forceinline__ void load_block(const uint16_t* __restrict__ p, uint32_t (&x)[16]) {
   const uint4* v = reinterpret_cast<const uint4*>(p);

@@ -49,6 +49,30 @@ hipError_t launch_kv_write(const void* k, int64_t k_stride, const void* v, int64
 hipError_t launch_kv_read(const void* cache, int64_t num_pages, int64_t P, int64_t heads, int64_t D,
                           const int64_t* slots, int64_t T, void* k, void* v, hipStream_t st);
 
+struct KvAppendArgs {
+  const uint16_t *q, *k, *v;
+  const int32_t* positions;
+  const int64_t* slots;
+  uint8_t* cache;
+  const float *q_weight, *k_weight, *inv_freq;
+  uint16_t* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, num_slots;
+  int T, Hq, H, D, log2_page, rot, pairs;
+  float eps, rope_scale;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st);
+
+struct VerifyArgs {
+  const float *p, *q;  // target's and draft's probabilities (q may be null)
+  int64_t p_stride, q_stride;
+  const int32_t *tokens, *cu_q, *kv_lens;
+  const float *accept, *sample;
+  int32_t *out, *accepted, *new_lens;
+  int T, B, V;
+};
+size_t verify_workspace_bytes(int64_t B, int64_t V);
+hipError_t launch_verify(const VerifyArgs& a, void* workspace, hipStream_t st);
+
 struct KvAttnArgs {
   const uint16_t* q;
   const uint8_t* cache;

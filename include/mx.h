@@ -487,13 +487,13 @@ enum { MX_ROPE_HALVES = 0, MX_ROPE_PAIRS = 1 };
  * What stands between the projection to queries, keys and values and mx_kv_attention, in one pass:
  * norms of each head, rotation by position, and the keys and values into the cache. For every head x
  * [D] of row t's queries and keys:
- *   y = x * weight / sqrt(mean(x^2) + eps)      (y = x where weight is NULL);
+ *   y = x * weight / sqrt(max(mean(x^2) + eps, 2^-126))      (y = x where weight is NULL);
  *   element pairs (a, b) of the first `rot` elements, number i of rot / 2 of them, become
  *   (a cos - b sin, a sin + b cos) with the angle positions[t] * inv_freq[i], formed in FP64, and cos
  *   and sin times rope_scale.
- * Queries are worked out in FP32 and rounded once to bf16, to q_out. Keys are worked out in FP64 and
- * rounded to FP32, values are taken as they are, and both are quantized with the rule at the top of
- * this file into slot slots[t] of the cache, as mx_kv_write does.
+ * Queries are worked out in FP32 (the angles and norms past its range in FP64) and rounded once to
+ * bf16, to q_out. Keys are quantized as FP64 arithmetic, rounded to FP32, has them, values as they are,
+ * both with the rule at the top of this file into slot slots[t] of the cache, as mx_kv_write does.
  *  q_bf16, k_bf16, v_bf16: row t's heads_q * D (heads * D) values at element t * q_stride (k_stride,
  *    v_stride); q_out likewise with q_out_stride >= heads_q * D. Strides are multiples of 8. q_out may
  *    be q_bf16 itself (with the same stride) and must not overlap any input otherwise.

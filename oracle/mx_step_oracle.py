@@ -85,7 +85,8 @@ def norm_rotate(x, positions, weight, eps, inv_freq, pairs, rope_scale=1.0):
     magnitudes of the one or two terms that each element of y is made of."""
     x = np.asarray(x, dtype=np.float64)
     if weight is not None:
-        x = x / np.sqrt((x * x).mean(axis=-1, keepdims=True) + np.float64(np.float32(eps))) * np.asarray(weight, dtype=np.float64)
+        mean = (x * x).mean(axis=-1, keepdims=True) + np.float64(np.float32(eps))
+        x = x / np.sqrt(np.maximum(mean, 2.0 ** -126)) * np.asarray(weight, dtype=np.float64)
     y, size = x.copy(), np.abs(x)
     if inv_freq is not None and len(inv_freq):
         n = len(inv_freq)
@@ -100,11 +101,14 @@ def norm_rotate(x, positions, weight, eps, inv_freq, pairs, rope_scale=1.0):
 
 
 def query_bound(y, size):
-    """How far a query may be: in FP32, with u = 2^-24, the norm's factor (rounded once, 2 u with its
-    own error), its product with the element and the weight (2 u), the rounded cosine and the product
-    (2 u), the sum (u): 7 u of each term, 8 allowed for the second order; then half a step of bf16,
-    2^-8 of the value (2^-134 among its subnormals)."""
-    return (2.0 ** -8 * np.abs(y) + 8 * 2.0 ** -24 * size) * (1 + 2.0 ** -8) + 2.0 ** -133
+    """How far a query may be: in FP32, with u = 2^-24, each of its two terms by its coefficient, cosine
+    or sine (2 u) times rope_scale and weight (2 u), and by its product (u, one of the two); their sum
+    (u); the norm's factor: the sum of squares, 8 fused products in a lane and up to 5 sums over lanes,
+    all of one sign, 13 u, of which the root takes half; the mean and eps in one fused product (u, half),
+    the root itself (2 u); the product with it (u). In all 6 + 7 + 2 + 1 = 16 u of the terms' magnitudes,
+    20 allowed for the second order and 1 / D; then half a step of bf16, 2^-8 of the value (2^-134 among
+    its subnormals)."""
+    return (2.0 ** -8 * np.abs(y) + 20 * 2.0 ** -24 * size) * (1 + 2.0 ** -8) + 2.0 ** -133
 
 
 def append(cache, k, v_bits, positions, slots, page, weight, eps, inv_freq, pairs, rope_scale=1.0):

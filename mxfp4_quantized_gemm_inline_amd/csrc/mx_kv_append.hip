@@ -391,7 +391,7 @@ template <int D, bool kPairs>
 hipError_t launch(const KvAppendArgs& a, hipStream_t st) {
   using Tile = AppendTile<D>;
   constexpr int kMost = 1 << 21;  // rows of a launch, which holds fewer than 2^32 threads
-  constexpr int kGroups = 2048;   // of queries, and of keys or values, wanted
+  constexpr int kGroups = 512;    // of queries, and of keys or values, wanted
   for (int64_t first = 0; first < a.T; first += kMost) {
     const int rows = (int)min(a.T - first, (int64_t)kMost);
     AppendGrid g;

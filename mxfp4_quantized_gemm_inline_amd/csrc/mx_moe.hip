@@ -9,142 +9,357 @@ namespace {
 
 // ------------------------------------------------------------------------------- route
 //
-// Keys: what is compared is an FP64 number whose low 10 mantissa bits are replaced by the expert's
-// number, so that the larger of two keys is the larger score or, of equal ones, the lower expert,
-// and one maximum brings value and place together. The 42 bits above hold a bf16 or FP32 logit
-// exactly, and a sum of score and bias to 2^-42 of it.
-
-constexpr double kNone = -__builtin_inf();
-
-__device__ __forceinline__ double key_of(double c, int i) {
-  c = fmin(fmax(c + 0.0, -1e300), 1e300);  // -0 becomes 0; an infinite key would be a NaN with the number in it
-  const uint64_t b = __builtin_bit_cast(uint64_t, c);
-  return __builtin_bit_cast(double, (b & ~1023ull) | (uint64_t)(b >> 63 ? i : 1023 - i));
-}
-__device__ __forceinline__ int index_of(double key) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, key);
-  return b >> 63 ? (int)(b & 1023) : 1023 - (int)(b & 1023);
-}
-__device__ __forceinline__ double value_of(double key) {
-  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~1023ull);
-}
-
-__device__ __forceinline__ double wave_max(double x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x = fmax(x, __shfl_xor(x, d));
-  return x;
-}
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-  return x;
-}
-
-__device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t t, int e) {
-  const int64_t at = t * a.stride + e;
-  if (a.f32) return static_cast<const float*>(a.logits)[at];
-  return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(a.logits)[at] << 16);
-}
+// A wave per token, experts over its lanes. Keys: what is compared is a number whose low bits are
+// replaced by the expert's, so that the larger of two keys is the larger score or, of equal ones, the
+// lower expert, and no two are equal. bf16 logits that are compared as they are: 32 bits, the logit's
+// 16 in order above the expert. Otherwise FP64: the 42 bits above the expert hold an FP32 logit exactly,
+// and a sum of score and bias to 2^-42 of it.
+//
+// The topk largest of E keys without sorting them: the lanes' largest keys are bisected for a bound that
+// at least topk of them reach, so that the topk largest of all reach it too; what reaches it (a few more
+// than topk, as a rule) is put one to a lane, and each is ranked by comparing it with all of them. Where
+// more than 64 reach the bound (rows of equal logits, the largest all in a few lanes) the largest is
+// taken topk times instead.
 
 constexpr int kRouteWaves = 4;
+constexpr int kBisections = 14;
 
-// A wave per token, experts spread over the lanes.
-__global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a) {
-  __shared__ double vals[kRouteWaves][1024];
+template <int kControl, int kRows = 0xF>
+__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)x, kControl, kRows, 0xF, false);
+}
+template <int kControl, int kRows = 0xF>
+__device__ __forceinline__ double dpp(double old, double x) {
+  const uint2 o = __builtin_bit_cast(uint2, old), u = __builtin_bit_cast(uint2, x);
+  return __builtin_bit_cast(double, make_uint2(dpp<kControl, kRows>(o.x, u.x), dpp<kControl, kRows>(o.y, u.y)));
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)x, lane); }
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint2 u = __builtin_bit_cast(uint2, x);
+  return __builtin_bit_cast(double, make_uint2(lane_value(u.x, lane), lane_value(u.y, lane)));
+}
+// op over the wave, the same in every lane: within rows of 16, then over the rows, to lane 63. `none`:
+// the operation's neutral element.
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_reduce(T x, T none, Op op) {
+  x = op(x, dpp<0x111>(none, x));       // a lane 1 below
+  x = op(x, dpp<0x112>(none, x));       // 2
+  x = op(x, dpp<0x114>(none, x));       // 4
+  x = op(x, dpp<0x118>(none, x));       // 8
+  x = op(x, dpp<0x142, 0xA>(none, x));  // the row below's last lane
+  x = op(x, dpp<0x143, 0xC>(none, x));  // the lower half's
+  return lane_value(x, 63);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  return wave_reduce(x, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ double wave_max(double x) {
+  return wave_reduce(x, -__builtin_inf(), [](double a, double b) { return fmax(a, b); });
+}
+__device__ __forceinline__ double wave_sum(double x) {
+  return wave_reduce(x, 0.0, [](double a, double b) { return a + b; });
+}
+
+// exp(x) for x <= 0 (-inf gives 0), in FP64: 2^n times the series of exp(r), |r| <= log(2) / 2, up to
+// r^13, whose next term is below 2^-57.
+__device__ __forceinline__ double exp_of(double x) {
+  x = fmax(x, -800.0);  // below the least subnormal
+  const double n = rint(x * 1.44269504088896340736);
+  double r = fma(-n, 0.693147180559945286227, x);
+  r = fma(-n, 2.31904681384629955842e-17, r);
+  double y = 1.0 / 6227020800.0;
+  y = fma(y, r, 1.0 / 479001600.0);
+  y = fma(y, r, 1.0 / 39916800.0);
+  y = fma(y, r, 1.0 / 3628800.0);
+  y = fma(y, r, 1.0 / 362880.0);
+  y = fma(y, r, 1.0 / 40320.0);
+  y = fma(y, r, 1.0 / 5040.0);
+  y = fma(y, r, 1.0 / 720.0);
+  y = fma(y, r, 1.0 / 120.0);
+  y = fma(y, r, 1.0 / 24.0);
+  y = fma(y, r, 1.0 / 6.0);
+  y = fma(y, r, 0.5);
+  y = fma(y, r, 1.0);
+  y = fma(y, r, 1.0);
+  return ldexp(y, (int)n);
+}
+__device__ __forceinline__ double sigmoid_of(double x) {
+  const double e = exp_of(-fabs(x)), d = 1.0 + e;
+  double r = __builtin_amdgcn_rcp(d);  // 1 <= d <= 2: two steps of Newton give all bits
+  r = fma(r, fma(-d, r, 1.0), r);
+  r = fma(r, fma(-d, r, 1.0), r);
+  return x >= 0 ? r : e * r;
+}
+
+__device__ __forceinline__ uint32_t in_order(uint32_t bits) { return bits ^ (bits >> 31 ? 0xFFFFFFFFu : 0x80000000u); }
+__device__ __forceinline__ uint32_t out_of_order(uint32_t x) { return x ^ (x >> 31 ? 0x80000000u : 0xFFFFFFFFu); }
+
+// Keys of 32 bits. kNone is below every key; coarse() keeps the order (not strictly), reaching() is the
+// least key of a coarse value.
+struct Key32 {
+  typedef uint32_t T;
+  static constexpr T kNone = 0;
+  static __device__ __forceinline__ T of(float logit, int e) {  // a bf16 value above -inf
+    return (in_order(__builtin_bit_cast(uint32_t, logit + 0.f)) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e);
+  }
+  static __device__ __forceinline__ int expert(T k) { return 0xFFFF - (int)(k & 0xFFFFu); }
+  static __device__ __forceinline__ float logit(T k) { return __builtin_bit_cast(float, out_of_order(k & 0xFFFF0000u) & 0xFFFF0000u); }
+  static __device__ __forceinline__ T larger(T a, T b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t coarse(T k) { return k; }
+  static __device__ __forceinline__ T reaching(uint32_t c) { return c; }
+};
+struct Key64 {
+  typedef double T;
+  static constexpr T kNone = -__builtin_inf();
+  static __device__ __forceinline__ T of(double c, int e) {
+    c = fmin(fmax(c + 0.0, -1e300), 1e300);  // -0 becomes 0; an infinite key would be a NaN with the number in it
+    const uint64_t b = __builtin_bit_cast(uint64_t, c);
+    return __builtin_bit_cast(double, (b & ~1023ull) | (uint64_t)(b >> 63 ? e : 1023 - e));
+  }
+  static __device__ __forceinline__ int expert(T k) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, k);
+    return b >> 63 ? (int)(b & 1023) : 1023 - (int)(b & 1023);
+  }
+  static __device__ __forceinline__ double value(T k) {
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~1023ull);
+  }
+  static __device__ __forceinline__ float logit(T k) { return (float)value(k); }
+  static __device__ __forceinline__ T larger(T a, T b) { return fmax(a, b); }
+  static __device__ __forceinline__ uint32_t coarse(T k) { return in_order((uint32_t)(__builtin_bit_cast(uint64_t, k) >> 32)); }
+  static __device__ __forceinline__ T reaching(uint32_t c) {
+    const uint32_t hi = out_of_order(c);
+    if (hi >= 0xFFF00000u) return kNone;  // the bits would be a NaN's
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | (hi >> 31 ? 0xFFFFFFFFu : 0u));
+  }
+};
+
+__device__ __forceinline__ float load_logit(const uint16_t* p, int64_t at) {
+  return __builtin_bit_cast(float, (uint32_t)p[at] << 16);
+}
+__device__ __forceinline__ float load_logit(const float* p, int64_t at) { return p[at]; }
+__device__ __forceinline__ void load4(float (&x)[4], const uint16_t* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  x[0] = __builtin_bit_cast(float, u.x << 16);
+  x[1] = __builtin_bit_cast(float, u.x & 0xFFFF0000u);
+  x[2] = __builtin_bit_cast(float, u.y << 16);
+  x[3] = __builtin_bit_cast(float, u.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load4(float (&x)[4], const float* p) {
+  const float4 u = *reinterpret_cast<const float4*>(p);
+  x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+}
+
+// What the host works out: each group has `lanes` neighbouring lanes (all 64 without groups).
+struct RouteShape {
+  int lanes, size;  // of a group: lanes, experts
+};
+
+// L: the logits' type. V: experts a lane, W of them neighbours (4: loaded together). Experts of a group
+// lie over its lanes in turn, W at a time.
+template <typename Key, typename L, int V, int W>
+__global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, RouteShape g) {
+  typedef typename Key::T T;
+  constexpr bool k64 = sizeof(T) == 8;
+  constexpr float kLargest = sizeof(L) == 2 ? 0x1.FEp127f : 0x1.FFFFFEp127f;  // the logits' type's
+  __shared__ T found[kRouteWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int rows = a.num_rows ? *a.num_rows : a.T;
-  for (int64_t t0 = (int64_t)blockIdx.x * kRouteWaves; t0 < a.T; t0 += (int64_t)gridDim.x * kRouteWaves) {
-  const int64_t t = t0 + w;
-  const bool live = t < a.T && t < rows;
-  constexpr int V = 16;
-  double key[V];
-  double top = kNone, sum = 0;
-  bool ok[V];
-  double x[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * 64 + lane;
-    float l = live && e < a.E ? load_logit(a, t, e) : -__builtin_inff();
-    if (a.bias && e < a.E && !(a.bias[e] > -__builtin_inff())) l = -__builtin_inff();
-    ok[v] = l > -__builtin_inff();
-    x[v] = ok[v] ? (double)fminf(l, 3.402823466e38f) : kNone;
-    top = fmax(top, x[v]);
-  }
-  const bool scored = a.bias || (a.groups > 1 && a.group_top == 2);
+  const int rows = a.num_rows ? min(*a.num_rows, a.T) : a.T;
+  const int my_group = lane / g.lanes, r = lane % g.lanes;
+  const L* logits = static_cast<const L*>(a.logits);
+  const bool scored = k64 && (a.bias || (a.groups > 1 && a.group_top == 2));
   const bool whole = !a.sigmoid && (scored || !a.renormalize);  // the softmax's sum over all experts
-  if (!a.sigmoid) top = wave_max(top);
-  double p[V];
-  if (scored || whole) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      p[v] = !ok[v] ? 0.0 : a.sigmoid ? 1 / (1 + exp(-x[v])) : exp(x[v] - top);
-      sum += p[v];
-    }
-    if (whole) {
-      sum = wave_sum(sum);
-#pragma unroll
-      for (int v = 0; v < V; ++v) p[v] /= sum;
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * 64 + lane;
-    key[v] = !ok[v] ? kNone : key_of(a.bias ? p[v] + (double)a.bias[e] : x[v], e);
-  }
-  if (a.groups > 1) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = v * 64 + lane;
-      if (e < a.E) vals[w][e] = !ok[v] ? kNone : a.bias || a.group_top == 1 ? value_of(key[v]) : p[v];
-    }
-    __syncthreads();
-    const int gs = a.E / a.groups;
-    double best = kNone, second = kNone;
-    if (lane < a.groups)
-      for (int i = 0; i < gs; ++i) {
-        const double y = vals[w][lane * gs + i];
-        second = fmax(second, fmin(best, y));
-        best = fmax(best, y);
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + w; t < a.T; t += (int64_t)gridDim.x * kRouteWaves) {
+    if (t >= rows) {
+      if (lane < a.topk) {
+        a.ids[t * a.topk + lane] = -1;
+        a.weights[t * a.topk + lane] = 0.f;
       }
-    if (a.group_top == 2 && second > kNone) best += second;
-    const double mine = best > kNone ? key_of(best, lane) : kNone;
-    int before = 0;
-    for (int g = 0; g < a.groups; ++g) before += __shfl(mine, g) > mine;
-    const uint64_t kept = __ballot(mine > kNone && before < a.topk_groups);
+      continue;
+    }
+    // an expert's place in its group, and its number
+    const auto place = [&](int v) { return (v / W * g.lanes + r) * W + v % W; };
+    const auto number = [&](int v) { return my_group * g.size + place(v); };
+    const auto has = [&](int v) { return my_group < a.groups && place(v) < g.size; };
+    float x[V];  // -inf: never chosen
+    const L* row = logits + t * a.stride;
+#pragma unroll
+    for (int v = 0; v < V; v += W) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[v + i] = -__builtin_inff();
+      if (has(v)) {
+        if constexpr (W == 4) {
+          float y[4];
+          load4(y, row + number(v));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[v + i] = y[i];
+        } else {
+          x[v] = load_logit(row, number(v));
+        }
+      }
+    }
+    float bias[V];
+    if (k64 && a.bias) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        bias[v] = has(v) ? a.bias[number(v)] : 0.f;
+        if (!(bias[v] > -__builtin_inff())) x[v] = -__builtin_inff();
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = x[v] > -__builtin_inff() ? fminf(x[v], kLargest) : -__builtin_inff();  // NaN: -inf
+    double top = 0, sum = 1;
+    double p[V];
+    if (whole) {
+      float m = -kLargest;
+#pragma unroll
+      for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
+      top = (double)__builtin_bit_cast(float, out_of_order(wave_max(in_order(__builtin_bit_cast(uint32_t, m)))));
+      sum = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        p[v] = exp_of((double)x[v] - top);
+        sum += p[v];
+      }
+      sum = wave_sum(sum);
+    }
+    if (scored) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[v] = a.sigmoid ? sigmoid_of((double)x[v]) : p[v] / sum;
+    }
+    T key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * 64 + lane;
-      if (e < a.E && !(kept >> (e / gs) & 1)) key[v] = kNone;
+      if constexpr (k64) key[v] = Key::of(a.bias ? p[v] + (double)bias[v] : (double)x[v], number(v));
+      else key[v] = Key::of(x[v], number(v));
+      if (!(x[v] > -__builtin_inff())) key[v] = Key::kNone;
+    }
+    if (a.groups > 1) {
+      // each lane its group's key: the value, and of equal ones the lower group
+      T best = Key::kNone;
+      if constexpr (k64) {
+        double one = Key64::kNone, two = Key64::kNone;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const double y = !(x[v] > -__builtin_inff()) ? Key64::kNone : a.bias || a.group_top == 1 ? Key64::value(key[v]) : p[v];
+          two = fmax(two, fmin(one, y));
+          one = fmax(one, y);
+        }
+        for (int d = 1; d < g.lanes; d <<= 1) {
+          const double y = __shfl_xor(one, d), z = __shfl_xor(two, d);
+          two = fmax(fmax(two, z), fmin(one, y));
+          one = fmax(one, y);
+        }
+        if (a.group_top == 2 && two > Key64::kNone) one += two;
+        if (one > Key64::kNone) best = Key64::of(one, my_group);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) best = max(best, key[v]);
+        for (int d = 1; d < g.lanes; d <<= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d));
+        if (best) best = (best & 0xFFFF0000u) | (uint32_t)(0xFFFF - my_group);
+      }
+      int before = 0;
+      for (int i = 0; i < a.groups; ++i) before += lane_value(best, i * g.lanes) > best ? 1 : 0;
+      if (before >= a.topk_groups) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = Key::kNone;
+      }
+    }
+    // the bound
+    T mine = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) mine = Key::larger(mine, key[v]);
+    const uint32_t c = Key::coarse(mine);
+    uint32_t lo = 0, hi = wave_max(c);
+    lo = ~wave_max(~c);
+    for (int i = 0; i < kBisections && lo < hi; ++i) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      const int n = (int)__popcll(__ballot(c >= mid));
+      if (n >= a.topk) lo = mid; else hi = mid - 1;
+      if (n == a.topk) break;
+    }
+    const T bound = Key::reaching(lo);
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) n += (int)__popcll(__ballot(key[v] >= bound && key[v] > Key::kNone));
+    T chosen = Key::kNone;
+    int rank = lane;
+    if (n <= 64) {
+      int at = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool is = key[v] >= bound && key[v] > Key::kNone;
+        const uint64_t all = __ballot(is);
+        if (is) found[w][at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] = key[v];
+        at += (int)__popcll(all);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are in order
+      if (lane < n) chosen = found[w][lane];
+      rank = 0;
+      for (int i = 0; i < n; ++i) rank += lane_value(chosen, i) > chosen ? 1 : 0;
+      if (lane >= n) rank = lane;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    } else {
+      for (int i = 0; i < a.topk; ++i) {
+        T best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = Key::larger(best, key[v]);
+        best = wave_max(best);
+        if (lane == i) chosen = best;
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = key[v] == best ? Key::kNone : key[v];
+      }
+    }
+    // weights
+    const bool is = rank < a.topk && chosen > Key::kNone;
+    int id = -1;
+    double s = 0;
+    double l = Key64::kNone;
+    if (is) {
+      id = Key::expert(chosen);
+      l = (double)(k64 && a.bias ? fminf(load_logit(row, id), kLargest) : Key::logit(chosen));
+    }
+    if (!a.sigmoid && !whole) top = fmax(wave_max(l), -(double)kLargest);
+    if (is) {
+      s = a.sigmoid ? sigmoid_of(l) : exp_of(l - top);
+      if (whole) s /= sum;
+    }
+    if (a.renormalize) {
+      const double all = wave_sum(s);
+      s = all > 0 ? s / all : 0;
+    }
+    if (rank < a.topk) {
+      a.ids[t * a.topk + rank] = id;
+      a.weights[t * a.topk + rank] = (float)(s * (double)a.scale);
     }
   }
-  double chosen = kNone;
-  for (int i = 0; i < a.topk; ++i) {
-    double best = kNone;
-#pragma unroll
-    for (int v = 0; v < V; ++v) best = fmax(best, key[v]);
-    best = wave_max(best);
-    if (lane == i) chosen = best;
-#pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = key[v] == best ? kNone : key[v];
+}
+
+template <typename Key, typename L, int V, int W>
+hipError_t route(const RouteArgs& a, const RouteShape& g, hipStream_t st) {
+  const int64_t groups = ((int64_t)a.T + kRouteWaves - 1) / kRouteWaves;
+  hipLaunchKernelGGL((k_moe_route<Key, L, V, W>), dim3((unsigned)min(groups, (int64_t)1 << 20)), dim3(64 * kRouteWaves), 0, st, a, g);
+  return hipGetLastError();
+}
+
+template <typename Key, typename L>
+hipError_t route(const RouteArgs& a, hipStream_t st) {
+  RouteShape g = {64, a.E / a.groups};
+  while (g.lanes > 64 / a.groups) g.lanes /= 2;
+  const int each = (g.size + g.lanes - 1) / g.lanes, fours = (g.size + 4 * g.lanes - 1) / (4 * g.lanes);
+  // four experts in one load where they lie so and it takes no more registers
+  const auto on = [](uint64_t x) { return x % (4 * sizeof(L)) == 0; };
+  const bool w4 = g.size % 4 == 0 && a.E % 4 == 0 && on((uint64_t)a.logits) && on((uint64_t)a.stride * sizeof(L)) && each > 2;
+  if (w4 && fours <= 4) {
+    if (fours == 1) return route<Key, L, 4, 4>(a, g, st);
+    if (fours == 2) return route<Key, L, 8, 4>(a, g, st);
+    return route<Key, L, 16, 4>(a, g, st);
   }
-  const bool has = lane < a.topk && chosen > kNone;
-  const int id = has ? index_of(chosen) : -1;
-  double s = 0;
-  if (has) {
-    const double l = fminf(load_logit(a, t, id), 3.402823466e38f);
-    s = a.sigmoid ? 1 / (1 + exp(-l)) : exp(l - top);
-    if (whole) s /= sum;
-  }
-  if (a.renormalize) {
-    const double all = wave_sum(s);
-    s = all > 0 ? s / all : 0;
-  }
-  if (t < a.T && lane < a.topk) {
-    a.ids[t * a.topk + lane] = id;
-    a.weights[t * a.topk + lane] = (float)(s * (double)a.scale);
-  }
-  __syncthreads();
-  }
+  if (each == 1) return route<Key, L, 1, 1>(a, g, st);
+  if (each == 2) return route<Key, L, 2, 1>(a, g, st);
+  if (each <= 4) return route<Key, L, 4, 1>(a, g, st);
+  if (each <= 8) return route<Key, L, 8, 1>(a, g, st);
+  if (each <= 16) return route<Key, L, 16, 1>(a, g, st);
+  return route<Key, L, 32, 1>(a, g, st);
 }
 
 // ------------------------------------------------------------------------------- sort
@@ -291,9 +506,9 @@ __global__ __launch_bounds__(64 * W) void k_moe_sort_place(SortArgs a, int chunk
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(k_moe_route, dim3((unsigned)min((a.T + (int64_t)kRouteWaves - 1) / kRouteWaves, (int64_t)1 << 20)), dim3(64 * kRouteWaves), 0,
-                     st, a);
-  return hipGetLastError();
+  if (a.f32) return route<Key64, float>(a, st);
+  if (a.bias || (a.groups > 1 && a.group_top == 2)) return route<Key64, uint16_t>(a, st);
+  return route<Key32, uint16_t>(a, st);
 }
 
 size_t moe_sort_workspace_bytes(int64_t N, int64_t E) {

@@ -15,6 +15,7 @@ from . import mx_act_oracle as A
 from . import mx_kv_oracle as KV
 
 FLT_MAX = float(np.finfo(np.float32).max)
+BF16_MAX = 2.0 ** 128 - 2.0 ** 120
 
 
 # ------------------------------------------------------------------------------- routing
@@ -25,13 +26,15 @@ def truncated(x: np.ndarray) -> np.ndarray:
     return (x.view(np.uint64) & ~np.uint64(1023)).view(np.float64)
 
 
-def route(logits, topk, bias=None, sigmoid=False, groups=1, topk_groups=1, group_top=2, renormalize=True, scale=1.0, rows=None):
-    """(ids int32 [T, topk], weights float64 [T, topk]) token by token; logits are float32 values."""
+def route(logits, topk, bias=None, sigmoid=False, groups=1, topk_groups=1, group_top=2, renormalize=True, scale=1.0, rows=None,
+          largest=FLT_MAX):
+    """(ids int32 [T, topk], weights float64 [T, topk]) token by token; logits are float32 values of a type
+    whose largest number is `largest`."""
     logits = np.asarray(logits, dtype=np.float64)
     T, E = logits.shape
     ids, weights = np.full((T, topk), -1, np.int32), np.zeros((T, topk))
     for t in range(T if rows is None else max(0, min(T, rows))):
-        l = np.minimum(logits[t], FLT_MAX)
+        l = np.minimum(logits[t], largest)
         ok = l > -math.inf
         if bias is not None:
             with np.errstate(invalid="ignore"):

@@ -31,7 +31,7 @@ def _check_route(mx, logits, topk, f32, bias=None, lead=0, pad=0, rows=None, sig
     """logits: float32 values (bf16 ones unless f32); lead: elements before the first row, pad: between rows."""
     import torch
     T, E = logits.shape
-    want, weights = S.route(logits, topk, bias=bias, sigmoid=sigmoid, rows=rows, **kw)
+    want, weights = S.route(logits, topk, bias=bias, sigmoid=sigmoid, rows=rows, largest=S.FLT_MAX if f32 else S.BF16_MAX, **kw)
     home = np.full((lead + T * (E + pad),), np.nan, np.float32)
     view = home[lead:].reshape(T, E + pad)
     view[:, :E] = logits

@@ -16,13 +16,13 @@ namespace {
 // and a sum of score and bias to 2^-42 of it.
 //
 // The topk largest of E keys without sorting them: the lanes' largest keys are bisected for a bound that
-// at least topk of them reach, so that the topk largest of all reach it too; what reaches it (a few more
-// than topk, as a rule) is put one to a lane, and each is ranked by comparing it with all of them. Where
-// more than 64 reach the bound (rows of equal logits, the largest all in a few lanes) the largest is
-// taken topk times instead.
+// at least topk of them reach, and few more, so that the topk largest of all reach it too; what reaches
+// it is put one to a lane, and each is ranked by comparing it with all of them. Where more than 64 reach
+// the bound (rows of equal logits, the largest all in a few lanes) the largest is taken topk times
+// instead.
 
 constexpr int kRouteWaves = 4;
-constexpr int kBisections = 14;
+constexpr int kBisections = 14;  // at most: the lanes that reach the bound may be a quarter more than topk
 
 template <int kControl, int kRows = 0xF>
 __device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
@@ -49,6 +49,15 @@ __device__ __forceinline__ T wave_reduce(T x, T none, Op op) {
   x = op(x, dpp<0x142, 0xA>(none, x));  // the row below's last lane
   x = op(x, dpp<0x143, 0xC>(none, x));  // the lower half's
   return lane_value(x, 63);
+}
+// The sum over the lanes up to each.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x += dpp<0x111>(0u, x);
+  x += dpp<0x112>(0u, x);
+  x += dpp<0x114>(0u, x);
+  x += dpp<0x118>(0u, x);
+  x += dpp<0x142, 0xA>(0u, x);
+  return x + dpp<0x143, 0xC>(0u, x);
 }
 __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
   return wave_reduce(x, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
@@ -94,11 +103,11 @@ __device__ __forceinline__ double sigmoid_of(double x) {
 __device__ __forceinline__ uint32_t in_order(uint32_t bits) { return bits ^ (bits >> 31 ? 0xFFFFFFFFu : 0x80000000u); }
 __device__ __forceinline__ uint32_t out_of_order(uint32_t x) { return x ^ (x >> 31 ? 0x80000000u : 0xFFFFFFFFu); }
 
-// Keys of 32 bits. kNone is below every key; coarse() keeps the order (not strictly), reaching() is the
+// Keys of 32 bits. kNone is below every key, kLeast above it and none of them; coarse() keeps the order (not strictly), reaching() is the
 // least key of a coarse value.
 struct Key32 {
   typedef uint32_t T;
-  static constexpr T kNone = 0;
+  static constexpr T kNone = 0, kLeast = 1;
   static __device__ __forceinline__ T of(float logit, int e) {  // a bf16 value above -inf
     return (in_order(__builtin_bit_cast(uint32_t, logit + 0.f)) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e);
   }
@@ -110,7 +119,7 @@ struct Key32 {
 };
 struct Key64 {
   typedef double T;
-  static constexpr T kNone = -__builtin_inf();
+  static constexpr T kNone = -__builtin_inf(), kLeast = -1e301;
   static __device__ __forceinline__ T of(double c, int e) {
     c = fmin(fmax(c + 0.0, -1e300), 1e300);  // -0 becomes 0; an infinite key would be a NaN with the number in it
     const uint64_t b = __builtin_bit_cast(uint64_t, c);
@@ -149,196 +158,214 @@ __device__ __forceinline__ void load4(float (&x)[4], const float* p) {
   x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
 }
 
-// What the host works out: each group has `lanes` neighbouring lanes (all 64 without groups).
+// What the host works out: each group has `lanes` neighbouring lanes, a power of two of them.
 struct RouteShape {
   int lanes, size;  // of a group: lanes, experts
 };
 
 // L: the logits' type. V: experts a lane, W of them neighbours (4: loaded together). Experts of a group
-// lie over its lanes in turn, W at a time.
-template <typename Key, typename L, int V, int W>
-__global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, RouteShape g) {
+// lie over its lanes in turn, W at a time; without groups (kGroups false) all over all lanes.
+template <typename Key, typename L, int V, int W, bool kGroups>
+__global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, RouteShape g, int first_row) {
   typedef typename Key::T T;
   constexpr bool k64 = sizeof(T) == 8;
   constexpr float kLargest = sizeof(L) == 2 ? 0x1.FEp127f : 0x1.FFFFFEp127f;  // the logits' type's
-  __shared__ T found[kRouteWaves][64];
+  __shared__ __attribute__((aligned(16))) T found[kRouteWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int rows = a.num_rows ? min(*a.num_rows, a.T) : a.T;
-  const int my_group = lane / g.lanes, r = lane % g.lanes;
+  const int lanes = kGroups ? g.lanes : 64, size = kGroups ? g.size : a.E, groups = kGroups ? a.groups : 1;
+  const int my_group = kGroups ? lane / lanes : 0, r = kGroups ? lane % lanes : lane;
   const L* logits = static_cast<const L*>(a.logits);
-  const bool scored = k64 && (a.bias || (a.groups > 1 && a.group_top == 2));
+  const bool scored = k64 && (a.bias || (kGroups && a.group_top == 2));
   const bool whole = !a.sigmoid && (scored || !a.renormalize);  // the softmax's sum over all experts
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + w; t < a.T; t += (int64_t)gridDim.x * kRouteWaves) {
-    if (t >= rows) {
-      if (lane < a.topk) {
-        a.ids[t * a.topk + lane] = -1;
-        a.weights[t * a.topk + lane] = 0.f;
-      }
-      continue;
+  const int t = first_row + (int)blockIdx.x * kRouteWaves + w;
+  if (t >= a.T) return;
+  int32_t* ids = a.ids + (int64_t)t * a.topk;
+  float* weights = a.weights + (int64_t)t * a.topk;
+  if (t >= rows) {
+    if (lane < a.topk) {
+      ids[lane] = -1;
+      weights[lane] = 0.f;
     }
-    // an expert's place in its group, and its number
-    const auto place = [&](int v) { return (v / W * g.lanes + r) * W + v % W; };
-    const auto number = [&](int v) { return my_group * g.size + place(v); };
-    const auto has = [&](int v) { return my_group < a.groups && place(v) < g.size; };
-    float x[V];  // -inf: never chosen
-    const L* row = logits + t * a.stride;
+    return;
+  }
+  // an expert's place in its group, and its number
+  const auto place = [&](int v) { return (v / W * lanes + r) * W + v % W; };
+  const auto number = [&](int v) { return my_group * size + place(v); };
+  const auto has = [&](int v) { return my_group < groups && place(v) < size; };
+  float x[V];  // -inf and NaN: never chosen
+  const L* row = logits + t * a.stride;
 #pragma unroll
-    for (int v = 0; v < V; v += W) {
+  for (int v = 0; v < V; v += W) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) x[v + i] = -__builtin_inff();
-      if (has(v)) {
-        if constexpr (W == 4) {
-          float y[4];
-          load4(y, row + number(v));
+    for (int i = 0; i < W; ++i) x[v + i] = -__builtin_inff();
+    if (has(v)) {
+      if constexpr (W == 4) {
+        float y[4];
+        load4(y, row + number(v));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[v + i] = y[i];
-        } else {
-          x[v] = load_logit(row, number(v));
-        }
-      }
-    }
-    float bias[V];
-    if (k64 && a.bias) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        bias[v] = has(v) ? a.bias[number(v)] : 0.f;
-        if (!(bias[v] > -__builtin_inff())) x[v] = -__builtin_inff();
+        for (int i = 0; i < 4; ++i) x[v + i] = y[i];
+      } else {
+        x[v] = load_logit(row, number(v));
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = x[v] > -__builtin_inff() ? fminf(x[v], kLargest) : -__builtin_inff();  // NaN: -inf
-    double top = 0, sum = 1;
-    double p[V];
-    if (whole) {
-      float m = -kLargest;
-#pragma unroll
-      for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
-      top = (double)__builtin_bit_cast(float, out_of_order(wave_max(in_order(__builtin_bit_cast(uint32_t, m)))));
-      sum = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        p[v] = exp_of((double)x[v] - top);
-        sum += p[v];
-      }
-      sum = wave_sum(sum);
-    }
-    if (scored) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p[v] = a.sigmoid ? sigmoid_of((double)x[v]) : p[v] / sum;
-    }
-    T key[V];
+  }
+  float bias[V];
+  if (k64 && a.bias) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if constexpr (k64) key[v] = Key::of(a.bias ? p[v] + (double)bias[v] : (double)x[v], number(v));
-      else key[v] = Key::of(x[v], number(v));
-      if (!(x[v] > -__builtin_inff())) key[v] = Key::kNone;
+      bias[v] = has(v) ? a.bias[number(v)] : 0.f;
+      if (!(bias[v] > -__builtin_inff())) x[v] = -__builtin_inff();
     }
-    if (a.groups > 1) {
-      // each lane its group's key: the value, and of equal ones the lower group
-      T best = Key::kNone;
-      if constexpr (k64) {
-        double one = Key64::kNone, two = Key64::kNone;
+  }
+  const auto masked = [&](int v) { return !(x[v] > -__builtin_inff()); };
+  double top = 0, sum = 1;
+  double p[V];
+  if (whole || scored) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const double y = !(x[v] > -__builtin_inff()) ? Key64::kNone : a.bias || a.group_top == 1 ? Key64::value(key[v]) : p[v];
-          two = fmax(two, fmin(one, y));
-          one = fmax(one, y);
-        }
-        for (int d = 1; d < g.lanes; d <<= 1) {
-          const double y = __shfl_xor(one, d), z = __shfl_xor(two, d);
-          two = fmax(fmax(two, z), fmin(one, y));
-          one = fmax(one, y);
-        }
-        if (a.group_top == 2 && two > Key64::kNone) one += two;
-        if (one > Key64::kNone) best = Key64::of(one, my_group);
-      } else {
+    for (int v = 0; v < V; ++v) x[v] = masked(v) ? -__builtin_inff() : fminf(x[v], kLargest);
+  }
+  if (whole) {
+    float m = -kLargest;
 #pragma unroll
-        for (int v = 0; v < V; ++v) best = max(best, key[v]);
-        for (int d = 1; d < g.lanes; d <<= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d));
-        if (best) best = (best & 0xFFFF0000u) | (uint32_t)(0xFFFF - my_group);
-      }
-      int before = 0;
-      for (int i = 0; i < a.groups; ++i) before += lane_value(best, i * g.lanes) > best ? 1 : 0;
-      if (before >= a.topk_groups) {
+    for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
+    top = (double)__builtin_bit_cast(float, out_of_order(wave_max(in_order(__builtin_bit_cast(uint32_t, m)))));
+    sum = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = Key::kNone;
-      }
+    for (int v = 0; v < V; ++v) {
+      p[v] = exp_of((double)x[v] - top);
+      sum += p[v];
     }
-    // the bound
-    T mine = key[0];
+    sum = wave_sum(sum);
+  }
+  if (scored) {
 #pragma unroll
-    for (int v = 1; v < V; ++v) mine = Key::larger(mine, key[v]);
-    const uint32_t c = Key::coarse(mine);
-    uint32_t lo = 0, hi = wave_max(c);
-    lo = ~wave_max(~c);
-    for (int i = 0; i < kBisections && lo < hi; ++i) {
-      const uint32_t mid = lo + (hi - lo + 1) / 2;
-      const int n = (int)__popcll(__ballot(c >= mid));
-      if (n >= a.topk) lo = mid; else hi = mid - 1;
-      if (n == a.topk) break;
-    }
-    const T bound = Key::reaching(lo);
-    int n = 0;
+    for (int v = 0; v < V; ++v) p[v] = a.sigmoid ? sigmoid_of((double)x[v]) : p[v] / sum;
+  }
+  T key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) n += (int)__popcll(__ballot(key[v] >= bound && key[v] > Key::kNone));
-    T chosen = Key::kNone;
-    int rank = lane;
-    if (n <= 64) {
-      int at = 0;
+  for (int v = 0; v < V; ++v) {
+    if constexpr (k64) key[v] = Key::of(a.bias ? p[v] + (double)bias[v] : (double)fminf(x[v], kLargest), number(v));
+    else key[v] = Key::of(fminf(x[v], kLargest), number(v));
+    if (masked(v)) key[v] = Key::kNone;
+  }
+  if (kGroups) {
+    // each lane its group's key: the value, and of equal ones the lower group
+    T best = Key::kNone;
+    if constexpr (k64) {
+      double one = Key64::kNone, two = Key64::kNone;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const bool is = key[v] >= bound && key[v] > Key::kNone;
-        const uint64_t all = __ballot(is);
-        if (is) found[w][at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] = key[v];
-        at += (int)__popcll(all);
+        const double y = masked(v) ? Key64::kNone : a.bias || a.group_top == 1 ? Key64::value(key[v]) : p[v];
+        two = fmax(two, fmin(one, y));
+        one = fmax(one, y);
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are in order
-      if (lane < n) chosen = found[w][lane];
-      rank = 0;
-      for (int i = 0; i < n; ++i) rank += lane_value(chosen, i) > chosen ? 1 : 0;
-      if (lane >= n) rank = lane;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int d = 1; d < lanes; d <<= 1) {
+        const double y = __shfl_xor(one, d), z = __shfl_xor(two, d);
+        two = fmax(fmax(two, z), fmin(one, y));
+        one = fmax(one, y);
+      }
+      if (a.group_top == 2 && two > Key64::kNone) one += two;
+      if (one > Key64::kNone) best = Key64::of(one, my_group);
     } else {
-      for (int i = 0; i < a.topk; ++i) {
-        T best = key[0];
 #pragma unroll
-        for (int v = 1; v < V; ++v) best = Key::larger(best, key[v]);
-        best = wave_max(best);
-        if (lane == i) chosen = best;
+      for (int v = 0; v < V; ++v) best = max(best, key[v]);
+      for (int d = 1; d < lanes; d <<= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d));
+      if (best) best = (best & 0xFFFF0000u) | (uint32_t)(0xFFFF - my_group);
+    }
+    int before = 0;
+    for (int i = 0; i < a.groups; ++i) before += lane_value(best, i * lanes) > best ? 1 : 0;
+    if (before >= a.topk_groups) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = key[v] == best ? Key::kNone : key[v];
-      }
+      for (int v = 0; v < V; ++v) key[v] = Key::kNone;
     }
-    // weights
-    const bool is = rank < a.topk && chosen > Key::kNone;
-    int id = -1;
-    double s = 0;
-    double l = Key64::kNone;
-    if (is) {
-      id = Key::expert(chosen);
-      l = (double)(k64 && a.bias ? fminf(load_logit(row, id), kLargest) : Key::logit(chosen));
+  }
+  // the bound
+  T mine = key[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) mine = Key::larger(mine, key[v]);
+  const uint32_t c = Key::coarse(mine);
+  uint32_t lo = 0, hi = wave_max(c);
+  lo = ~wave_max(~c);
+  for (int i = 0; i < kBisections && lo < hi; ++i) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    const int n = (int)__popcll(__ballot(c >= mid));
+    if (n < a.topk) {
+      hi = mid - 1;
+    } else {
+      lo = mid;
+      if (n <= a.topk + a.topk / 4) break;
     }
-    if (!a.sigmoid && !whole) top = fmax(wave_max(l), -(double)kLargest);
-    if (is) {
-      s = a.sigmoid ? sigmoid_of(l) : exp_of(l - top);
-      if (whole) s /= sum;
+  }
+  const T bound = Key::larger(Key::reaching(lo), Key::kLeast);
+  // what reaches it: how many of each lane's, and where they go
+  int mine_n = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) mine_n += key[v] >= bound ? 1 : 0;
+  const int upto = (int)wave_scan((uint32_t)mine_n), n = (int)lane_value((uint32_t)upto, 63);
+  T chosen = Key::kNone;
+  int rank = lane;
+  if (n <= 64) {
+    found[w][lane] = Key::kNone;
+    int at = upto - mine_n;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (key[v] >= bound) found[w][at++] = key[v];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are in order
+    chosen = found[w][lane];
+    int before = 0;
+    for (int i = 0; i < n; i += 4) {  // 16 bytes or 32 of the list, the same to every lane
+      const T k0 = found[w][i], k1 = found[w][i + 1], k2 = found[w][i + 2], k3 = found[w][i + 3];
+      before += (k0 > chosen) + (k1 > chosen) + (k2 > chosen) + (k3 > chosen);
     }
-    if (a.renormalize) {
-      const double all = wave_sum(s);
-      s = all > 0 ? s / all : 0;
+    if (lane < n) rank = before;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  } else {
+    for (int i = 0; i < a.topk; ++i) {
+      T best = key[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) best = Key::larger(best, key[v]);
+      best = wave_max(best);
+      if (lane == i) chosen = best;
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = key[v] == best ? Key::kNone : key[v];
     }
-    if (rank < a.topk) {
-      a.ids[t * a.topk + rank] = id;
-      a.weights[t * a.topk + rank] = (float)(s * (double)a.scale);
-    }
+  }
+  // weights
+  const bool is = rank < a.topk && chosen > Key::kNone;
+  int id = -1;
+  double s = 0;
+  double l = Key64::kNone;
+  if (is) {
+    id = Key::expert(chosen);
+    l = (double)(k64 && a.bias ? fminf(load_logit(row, id), kLargest) : Key::logit(chosen));
+  }
+  if (!a.sigmoid && !whole) top = lane_value(l, __builtin_ctzll(__ballot(rank == 0)));  // of the first, or none
+  if (is) {
+    s = a.sigmoid ? sigmoid_of(l) : exp_of(l - top);
+    if (whole) s /= sum;
+  }
+  if (a.renormalize) {
+    const double all = wave_sum(s);
+    s = all > 0 ? s / all : 0;
+  }
+  if (rank < a.topk) {
+    ids[rank] = id;
+    weights[rank] = (float)(s * (double)a.scale);
   }
 }
 
 template <typename Key, typename L, int V, int W>
 hipError_t route(const RouteArgs& a, const RouteShape& g, hipStream_t st) {
-  const int64_t groups = ((int64_t)a.T + kRouteWaves - 1) / kRouteWaves;
-  hipLaunchKernelGGL((k_moe_route<Key, L, V, W>), dim3((unsigned)min(groups, (int64_t)1 << 20)), dim3(64 * kRouteWaves), 0, st, a, g);
-  return hipGetLastError();
+  constexpr int kMost = 1 << 22;  // rows of a launch, which holds fewer than 2^32 threads
+  for (int64_t first = 0; first < a.T; first += kMost) {
+    const dim3 grid((unsigned)((min(a.T - first, (int64_t)kMost) + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
+    if (a.groups > 1) hipLaunchKernelGGL((k_moe_route<Key, L, V, W, true>), grid, block, 0, st, a, g, (int)first);
+    else hipLaunchKernelGGL((k_moe_route<Key, L, V, W, false>), grid, block, 0, st, a, g, (int)first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename Key, typename L>
@@ -348,7 +375,7 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
   const int each = (g.size + g.lanes - 1) / g.lanes, fours = (g.size + 4 * g.lanes - 1) / (4 * g.lanes);
   // four experts in one load where they lie so and it takes no more registers
   const auto on = [](uint64_t x) { return x % (4 * sizeof(L)) == 0; };
-  const bool w4 = g.size % 4 == 0 && a.E % 4 == 0 && on((uint64_t)a.logits) && on((uint64_t)a.stride * sizeof(L)) && each > 2;
+  const bool w4 = g.size % 4 == 0 && on((uint64_t)a.logits) && on((uint64_t)a.stride * sizeof(L)) && each > 2;
   if (w4 && fours <= 4) {
     if (fours == 1) return route<Key, L, 4, 4>(a, g, st);
     if (fours == 2) return route<Key, L, 8, 4>(a, g, st);

@@ -24,7 +24,7 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t st);
 struct SortArgs {
   const int32_t* ids;
   int32_t *offsets, *row_token, *token_rows;
-  int N, topk, first, E;
+  int N, topk, first, E, bits;  // bits: of an expert's number, E - 1 at most
 };
 size_t moe_sort_workspace_bytes(int64_t N, int64_t E);
 hipError_t launch_moe_sort(const SortArgs& a, void* workspace, hipStream_t st);

@@ -391,39 +391,186 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
 
 // ------------------------------------------------------------------------------- sort
 //
-// A stable counting sort. Every wave of a workgroup has its own part of the places, in order, and its
-// own counters in LDS: counted first, then set to where the wave's rows of each expert start, then
-// advanced 64 places at a time, lanes of one expert ranked by ballots over the number's bits.
-// Few places: one workgroup does it all. More: each workgroup counts its places, the counts of an
-// expert are summed up over the workgroups, each workgroup places its own.
+// A stable counting sort. A wave has a part of the places, in order, and a row of counters in LDS, which
+// it advances 64 places at a time, lanes of one expert ranked by ballots over the number's bits.
+// Up to kSortAll places one launch does it: each workgroup counts all places, what lies before its own
+// and behind them too, so that none waits for another. Beyond, a first launch ranks each place among its
+// workgroup's of the same expert (to token_rows) and counts those, a last one adds where they start; the
+// counts before a workgroup's are summed up there, or, where there are more than kSortSums workgroups,
+// by a launch between the two.
 
-constexpr int kSortOne = 16384;    // places of a single workgroup, at most
-constexpr int kSortChunk = 4096;   // places of one of several, at least
-constexpr int kSortChunks = 1024;  // workgroups, at most
-inline bool sort_one(int64_t N) { return N <= kSortOne; }
+constexpr int kSortAll = 16384;
+constexpr int kSortChunk = 2048;   // places of a workgroup of the others, or a multiple
+constexpr int kSortChunks = 1024;  // workgroups of those, at most
+constexpr int kSortSums = 64;
+constexpr int kEach = 8;           // places that a lane loads ahead
 inline int sort_chunk(int64_t N) {
   const int64_t each = (N + kSortChunks - 1) / kSortChunks;
-  return (int)(each <= kSortChunk ? kSortChunk : (each + 255) / 256 * 256);
+  return (int)((max(each, (int64_t)kSortChunk) + kSortChunk - 1) / kSortChunk * kSortChunk);
 }
 inline int sort_chunks(int64_t N) { return (int)((N + sort_chunk(N) - 1) / sort_chunk(N)); }
 
+// The expert of place n among this call's, -1 for others'.
 __device__ __forceinline__ int local_expert(const SortArgs& a, int n) {
   const uint32_t e = (uint32_t)a.ids[n] - (uint32_t)a.first;
   return e < (uint32_t)a.E ? (int)e : -1;
 }
 
-// counts: [E][chunks]
-__global__ __launch_bounds__(256) void k_moe_sort_count(SortArgs a, int chunk, int32_t* counts) {
-  __shared__ int32_t cnt[1024];
-  for (int e = threadIdx.x; e < a.E; e += 256) cnt[e] = 0;
+// Inclusive sum over the workgroup's threads; part: a word a wave.
+template <int W>
+__device__ __forceinline__ int group_scan(int x, int32_t* part) {
+  const int upto = (int)wave_scan((uint32_t)x), w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 63) part[w] = upto;
   __syncthreads();
-  const int n0 = (int)blockIdx.x * chunk, n1 = min(a.N, n0 + chunk);
-  for (int n = n0 + (int)threadIdx.x; n < n1; n += 256) {
-    const int e = local_expert(a, n);
-    if (e >= 0) atomicAdd(&cnt[e], 1);
+  int base = 0;
+  for (int i = 0; i < w; ++i) base += part[i];
+  return upto + base;
+}
+
+// at: each one's place among those of its expert (e, or -1 for none) that the wave has had, whose number
+// cnt[] holds. First lanes of the same expert by ballots over the bits of its number, then counters, then
+// what they were: none waits for another's way through LDS.
+template <int K>
+__device__ __forceinline__ void next_places(int (&at)[K], const int (&e)[K], int bits, int32_t* cnt) {
+  uint64_t same[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) same[i] = __ballot(e[i] >= 0);
+#pragma unroll 1
+  for (int b = 0; b < bits; ++b)
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const bool one = e[i] >> b & 1;
+      same[i] &= __ballot(one) ^ (one ? 0 : ~0ull);
+    }
+  int leader[K], base[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    at[i] = __builtin_amdgcn_mbcnt_hi((uint32_t)(same[i] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same[i], 0));
+    leader[i] = same[i] ? (int)__builtin_ctzll(same[i]) : 0;
+    base[i] = e[i] >= 0 && at[i] == 0 ? (int)__popcll(same[i]) : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+    if (base[i]) base[i] = atomicAdd(&cnt[e[i]], base[i]);
+#pragma unroll
+  for (int i = 0; i < K; ++i) at[i] = e[i] >= 0 ? __shfl(base[i], leader[i]) + at[i] : -1;
+}
+
+// W waves a workgroup, kSteps times 64 places a wave.
+template <int W, int kSteps>
+__global__ __launch_bounds__(64 * W) void k_moe_sort(SortArgs a) {
+  constexpr int kThreads = 64 * W, kExperts = 1024 / kThreads;  // experts a thread
+  constexpr int each = 64 * kSteps, share = W * each;
+  __shared__ int32_t cnt[W][1024];
+  __shared__ int32_t before[1024], behind[1024];
+  __shared__ int32_t part[W];
+  const int w = threadIdx.x >> 6;
+  const int n0 = (int)blockIdx.x * share, n1 = min(a.N, n0 + share);
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    before[e] = behind[e] = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) cnt[i][e] = 0;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += 256) counts[(int64_t)e * gridDim.x + blockIdx.x] = cnt[e];
+  for (int b0 = 0; b0 < a.N; b0 += kThreads * kEach) {
+    int e[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int n = b0 + kThreads * i + (int)threadIdx.x;
+      e[i] = n < a.N ? local_expert(a, n) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int n = b0 + kThreads * i + (int)threadIdx.x;
+      if (e[i] >= 0) atomicAdd(n < n0 ? &before[e[i]] : n >= n1 ? &behind[e[i]] : &cnt[(n - n0) / each][e[i]], 1);
+    }
+  }
+  __syncthreads();
+  int x[kExperts], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kExperts; ++i) {
+    const int e = (int)threadIdx.x * kExperts + i;
+    x[i] = 0;
+    if (e < a.E) {
+      x[i] = before[e] + behind[e];
+#pragma unroll
+      for (int j = 0; j < W; ++j) x[i] += cnt[j][e];
+    }
+    sum += x[i];
+  }
+  int run = group_scan<W>(sum, part) - sum;
+#pragma unroll
+  for (int i = 0; i < kExperts; ++i) {
+    const int e = (int)threadIdx.x * kExperts + i;
+    if (e < a.E) {
+      if (blockIdx.x == 0) a.offsets[e] = run;
+      int base = run + before[e];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const int c = cnt[j][e];
+        cnt[j][e] = base;
+        base += c;
+      }
+    }
+    run += x[i];
+  }
+  int R = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) R += part[i];
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = R;
+  __syncthreads();
+  int own[kSteps], at[kSteps];
+  const int m0 = n0 + w * each + (int)(threadIdx.x & 63);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) own[i] = m0 + 64 * i < n1 ? local_expert(a, m0 + 64 * i) : -1;
+  next_places(at, own, a.bits, cnt[w]);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int n = m0 + 64 * i;
+    if (at[i] >= 0) a.row_token[at[i]] = n / a.topk;
+    if (n < n1) a.token_rows[n] = at[i];
+  }
+  for (int r = R + (int)(blockIdx.x * kThreads + threadIdx.x); r < a.N; r += (int)gridDim.x * kThreads) a.row_token[r] = -1;
+}
+
+// token_rows: each place's number among this workgroup's of its expert; counts: how many of each,
+// [chunks][E], or with kScan [E][chunks].
+template <bool kScan>
+__global__ __launch_bounds__(256) void k_moe_sort_rank(SortArgs a, int chunk, int32_t* counts) {
+  __shared__ int32_t cnt[4][1024];
+  __shared__ int32_t sums[1024];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int e = threadIdx.x; e < a.E; e += 256) sums[e] = 0;
+  const int64_t n0 = (int64_t)blockIdx.x * chunk, n1 = min((int64_t)a.N, n0 + chunk);
+  for (int64_t s0 = n0; s0 < n1; s0 += kSortChunk) {
+    int e[kEach], at[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t n = s0 + (w * kEach + i) * 64 + lane;
+      e[i] = n < n1 ? local_expert(a, (int)n) : -1;
+    }
+    for (int i = lane; i < a.E; i += 64) cnt[w][i] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are in order
+    next_places(at, e, a.bits, cnt[w]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.E; i += 256) {
+      int base = sums[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = cnt[j][i];
+        cnt[j][i] = base;
+        base += c;
+      }
+      sums[i] = base;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t n = s0 + (w * kEach + i) * 64 + lane;
+      if (n < n1) a.token_rows[n] = e[i] >= 0 ? cnt[w][e[i]] + at[i] : -1;
+    }
+  }
+  for (int e = threadIdx.x; e < a.E; e += 256) counts[kScan ? (int64_t)e * gridDim.x + blockIdx.x : (int64_t)blockIdx.x * a.E + e] = sums[e];
 }
 
 // A wave per expert: counts become the sums before them, totals: [E] their sums.
@@ -432,102 +579,52 @@ __global__ __launch_bounds__(64) void k_moe_sort_scan(int32_t* counts, int chunk
   int base = 0;
   for (int c0 = 0; c0 < chunks; c0 += 64) {
     const int c = c0 + (int)threadIdx.x, x = c < chunks ? mine[c] : 0;
-    int s = x;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(s, d);
-      if ((int)threadIdx.x >= d) s += y;
-    }
-    if (c < chunks) mine[c] = base + s - x;
-    base += __shfl(s, 63);
+    const int upto = (int)wave_scan((uint32_t)x);
+    if (c < chunks) mine[c] = base + upto - x;
+    base += (int)lane_value((uint32_t)upto, 63);
   }
   if (threadIdx.x == 0) totals[blockIdx.x] = base;
 }
 
-// counts, totals: of the two kernels above, or null where this is the only workgroup.
-template <int W>
-__global__ __launch_bounds__(64 * W) void k_moe_sort_place(SortArgs a, int chunk, const int32_t* counts,
-                                                         const int32_t* totals) {
-  constexpr int kThreads = 64 * W, kEach = 1024 / kThreads;  // experts a thread
-  __shared__ int32_t cnt[W][1024];
-  __shared__ int32_t start[1025];
-  __shared__ int32_t part[W];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int n0 = (int)blockIdx.x * chunk, n1 = min(a.N, n0 + chunk), each = chunk / W;
-  const int w0 = n0 + w * each, w1 = min(n1, w0 + each);
-  for (int i = threadIdx.x; i < W * a.E; i += kThreads) cnt[i / a.E][i % a.E] = 0;
-  __syncthreads();
-  for (int n = w0 + lane; n < w1; n += 64) {
-    const int e = local_expert(a, n);
-    if (e >= 0) atomicAdd(&cnt[w][e], 1);
-  }
-  __syncthreads();
-  // where each expert's rows start
-  int x[kEach], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int e = (int)threadIdx.x * kEach + i;
-    x[i] = 0;
-    if (e < a.E) {
-      if (totals) {
-        x[i] = totals[e];
-      } else {
-        for (int j = 0; j < W; ++j) x[i] += cnt[j][e];
+template <bool kScan>
+__global__ __launch_bounds__(1024) void k_moe_sort_place(SortArgs a, int chunk, const int32_t* counts, const int32_t* totals) {
+  __shared__ int32_t start[1024];
+  __shared__ int32_t part[16];
+  const int e = threadIdx.x;  // an expert a thread
+  int all = 0, before = 0;
+  if (e < a.E) {
+    if (kScan) {
+      all = totals[e];
+      before = counts[(int64_t)e * gridDim.x + blockIdx.x];
+    } else {
+#pragma unroll 16
+      for (int c = 0; c < (int)gridDim.x; ++c) {
+        const int x = counts[c * a.E + e];
+        before += c < (int)blockIdx.x ? x : 0;
+        all += x;
       }
     }
-    sum += x[i];
   }
-  int run = sum;
+  const int run = group_scan<16>(all, part) - all;
+  if (e < a.E) {
+    start[e] = run + before;
+    if (blockIdx.x == 0) a.offsets[e] = run;
+  }
+  int R = 0;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(run, d);
-    if (lane >= d) run += y;
-  }
-  if (lane == 63) part[w] = run;
+  for (int i = 0; i < 16; ++i) R += part[i];
+  if (blockIdx.x == 0 && e == 0) a.offsets[a.E] = R;
   __syncthreads();
-  run -= sum;
-  for (int i = 0; i < w; ++i) run += part[i];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int e = (int)threadIdx.x * kEach + i;
-    if (e <= a.E) start[e] = run;
-    run += x[i];
-  }
-  if (threadIdx.x == kThreads - 1 && a.E == 1024) start[1024] = run;
-  __syncthreads();
-  const int R = start[a.E];
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    int base = start[e] + (counts ? counts[(int64_t)e * gridDim.x + blockIdx.x] : 0);
-    for (int i = 0; i < W; ++i) {
-      const int c = cnt[i][e];
-      cnt[i][e] = base;
-      base += c;
+  const int64_t n0 = (int64_t)blockIdx.x * chunk, n1 = min((int64_t)a.N, n0 + chunk);
+  for (int64_t n = n0 + threadIdx.x; n < n1; n += 1024) {
+    const int x = local_expert(a, (int)n);
+    if (x >= 0) {
+      const int row = start[x] + a.token_rows[n];
+      a.row_token[row] = (int)n / a.topk;
+      a.token_rows[n] = row;
     }
   }
-  if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e <= a.E; e += kThreads) a.offsets[e] = start[e];
-  __syncthreads();
-  for (int m0 = w0; m0 < w1; m0 += 64) {
-    const int n = m0 + lane;
-    const int e = n < w1 ? local_expert(a, n) : -1;
-    uint64_t same = __ballot(e >= 0);  // lanes of the same expert
-#pragma unroll
-    for (int b = 0; b < 10; ++b) {
-      const uint64_t one = __ballot(e >> b & 1);
-      same &= (e >> b & 1) ? one : ~one;
-    }
-    int row = -1;
-    if (e >= 0) {
-      const int rank = __popcll(same & ((1ull << lane) - 1));
-      int base = 0;
-      if (rank == 0) base = atomicAdd(&cnt[w][e], (int)__popcll(same));
-      row = __shfl(base, __builtin_ctzll(same)) + rank;
-      a.row_token[row] = n / a.topk;
-    }
-    if (n < w1) a.token_rows[n] = row;
-  }
-  for (int64_t r = (int64_t)R + blockIdx.x * kThreads + threadIdx.x; r < a.N; r += (int64_t)gridDim.x * kThreads)
-    a.row_token[r] = -1;
+  for (int64_t r = (int64_t)R + blockIdx.x * 1024 + threadIdx.x; r < a.N; r += (int64_t)gridDim.x * 1024) a.row_token[r] = -1;
 }
 
 }  // namespace
@@ -539,27 +636,35 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t st) {
 }
 
 size_t moe_sort_workspace_bytes(int64_t N, int64_t E) {
-  return sort_one(N) ? 0 : (size_t)(E * (sort_chunks(N) + 1)) * 4;
+  return N <= kSortAll ? 0 : (size_t)(E * (sort_chunks(N) + 1)) * 4;
 }
 
 hipError_t launch_moe_sort(const SortArgs& a, void* workspace, hipStream_t st) {
-  if (sort_one(a.N)) {
-    const int chunk = (a.N + 1023) / 1024 * 1024;
-    hipLaunchKernelGGL(k_moe_sort_place<16>, dim3(1), dim3(1024), 0, st, a, chunk, (const int32_t*)nullptr,
-                       (const int32_t*)nullptr);
+  if (a.N <= 1024) {
+    hipLaunchKernelGGL((k_moe_sort<4, 4>), dim3(1), dim3(256), 0, st, a);
+    return hipGetLastError();
+  }
+  if (a.N <= kSortAll) {
+    hipLaunchKernelGGL((k_moe_sort<16, 2>), dim3((unsigned)((a.N + 2047) / 2048)), dim3(1024), 0, st, a);
     return hipGetLastError();
   }
   const int chunk = sort_chunk(a.N), chunks = sort_chunks(a.N);
   int32_t* totals = static_cast<int32_t*>(workspace);
   int32_t* counts = totals + a.E;
-  hipLaunchKernelGGL(k_moe_sort_count, dim3((unsigned)chunks), dim3(256), 0, st, a, chunk, counts);
+  const dim3 grid((unsigned)chunks), block(256);
+  const bool scan = chunks > kSortSums;
+  if (scan) hipLaunchKernelGGL(k_moe_sort_rank<true>, grid, block, 0, st, a, chunk, counts);
+  else hipLaunchKernelGGL(k_moe_sort_rank<false>, grid, block, 0, st, a, chunk, counts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_moe_sort_scan, dim3((unsigned)a.E), dim3(64), 0, st, counts, chunks, totals);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_moe_sort_place<4>, dim3((unsigned)chunks), dim3(256), 0, st, a, chunk, (const int32_t*)counts,
-                     (const int32_t*)totals);
+  if (scan) {
+    hipLaunchKernelGGL(k_moe_sort_scan, dim3((unsigned)a.E), dim3(64), 0, st, counts, chunks, totals);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_moe_sort_place<true>, grid, dim3(1024), 0, st, a, chunk, (const int32_t*)counts, (const int32_t*)totals);
+  } else {
+    hipLaunchKernelGGL(k_moe_sort_place<false>, grid, dim3(1024), 0, st, a, chunk, (const int32_t*)counts, (const int32_t*)nullptr);
+  }
   return hipGetLastError();
 }
 

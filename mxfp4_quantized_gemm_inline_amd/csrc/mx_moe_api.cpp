@@ -65,7 +65,7 @@ mx_status mx_moe_sort(const int32_t* topk_ids, int64_t T, int64_t topk, int64_t 
   const mx_status d = mx::check_device();
   if (d != MX_OK) return d;
   const mx::SortArgs a = {topk_ids, expert_offsets, row_token, token_rows, (int)(T * topk), (int)topk, (int)first_expert,
-                          (int)E};
+                          (int)E, E > 1 ? 64 - __builtin_clzll((unsigned long long)(E - 1)) : 0};
   return from_hip(mx::launch_moe_sort(a, workspace, stream));
 }
 

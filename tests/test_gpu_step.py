@@ -440,7 +440,7 @@ def test_verify_at_the_borders_of_its_numbers():
                 _check_verify(mx, p, d, t2, cu, kv, 0 * accept, sample)
         # tables that leave the rows: clamped
         _check_verify(mx, p, q, tokens, [0, 4, 4, 9, 4000], kv, accept, sample)
-        _check_verify(mx, p, q, tokens, [-5, 2, 1, 3, 6], kv, accept, sample)
+        _check_verify(mx, p, q, tokens, [-5, 2, 2, 3, 6], kv, accept, sample)
 
 
 def test_verify_of_nothing_and_in_place():

@@ -70,24 +70,17 @@ __device__ __forceinline__ double wave_sum(double x) {
 }
 
 // exp(x) for x <= 0 (-inf gives 0), in FP64: 2^n times the series of exp(r), |r| <= log(2) / 2, up to
-// r^13, whose next term is below 2^-57.
+// r^13, whose next term is below 2^-57. Its terms come from memory by scalar loads: as literals each
+// would take instructions of its own in every use.
+__constant__ double kExpTerms[12] = {1.0 / 6227020800.0, 1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+                                     1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0, 0.5};
 __device__ __forceinline__ double exp_of(double x) {
   x = fmax(x, -800.0);  // below the least subnormal
   const double n = rint(x * 1.44269504088896340736);
-  double r = fma(-n, 0.693147180559945286227, x);
-  r = fma(-n, 2.31904681384629955842e-17, r);
-  double y = 1.0 / 6227020800.0;
-  y = fma(y, r, 1.0 / 479001600.0);
-  y = fma(y, r, 1.0 / 39916800.0);
-  y = fma(y, r, 1.0 / 3628800.0);
-  y = fma(y, r, 1.0 / 362880.0);
-  y = fma(y, r, 1.0 / 40320.0);
-  y = fma(y, r, 1.0 / 5040.0);
-  y = fma(y, r, 1.0 / 720.0);
-  y = fma(y, r, 1.0 / 120.0);
-  y = fma(y, r, 1.0 / 24.0);
-  y = fma(y, r, 1.0 / 6.0);
-  y = fma(y, r, 0.5);
+  const double r = fma(-n, 2.31904681384629955842e-17, fma(-n, 0.693147180559945286227, x));
+  double y = kExpTerms[0];
+#pragma unroll
+  for (int i = 1; i < 12; ++i) y = fma(y, r, kExpTerms[i]);
   y = fma(y, r, 1.0);
   y = fma(y, r, 1.0);
   return ldexp(y, (int)n);
@@ -238,9 +231,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
     }
     sum = wave_sum(sum);
   }
-  if (scored) {
+  if (scored && a.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) p[v] = a.sigmoid ? sigmoid_of((double)x[v]) : p[v] / sum;
+    for (int v = 0; v < V; ++v) p[v] = sigmoid_of((double)x[v]);
+  } else if (scored) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] /= sum;
   }
   T key[V];
 #pragma unroll

@@ -7,27 +7,21 @@ namespace mx {
 namespace {
 
 // Two launches. The first finds each request's first refused draft, every workgroup for itself (it is a
-// handful of numbers), and sums a slice of the row that the next token is drawn from; the second finds
-// the slice and then the token at which the running sum passes its number. Sums are FP64, in a fixed
-// order.
+// handful of numbers), and sums the row that the next token is drawn from, a chunk a wave; the second
+// finds the chunk and then the token at which the running sum passes its number. Sums are FP64, in a
+// fixed order.
 
-constexpr int kThreads = 256;
-constexpr int kAhead = 8;  // elements that a thread loads at once
-constexpr int kStep = kThreads * kAhead;
-constexpr int kMaxSlices = kThreads;  // one a thread of the second launch
-constexpr int kGroups = 1024;         // workgroups of the first, at least, where the slices are long enough
-constexpr int kBlock = 4096;          // elements that the second takes at a time: a slice, as a rule
-constexpr int kEach = kBlock / kThreads;
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kChunks = kThreads;  // of a row, at most: one a thread of the second launch
+constexpr int kStep = 1024;        // elements that a wave, or the second launch's workgroup, takes at a time
+constexpr int kAhead = kStep / 64, kEach = kStep / kThreads;
 
-// Elements of a slice: a multiple of kStep.
-inline int slice_of(int64_t B, int64_t V) {
-  const int64_t want = min(max(kGroups / B, (V + kBlock - 1) / kBlock), (int64_t)kMaxSlices);
-  const int64_t each = (V + want - 1) / want;
-  return (int)((each + kStep - 1) / kStep * kStep);
-}
-inline int slices_of(int64_t B, int64_t V) { return (int)((V + slice_of(B, V) - 1) / slice_of(B, V)); }
+// Elements of a chunk: a multiple of kStep. A row's first chunk begins up to 63 elements before it, where
+// a wave's loads are of whole lines also in rows of an odd length.
+inline int chunk_of(int64_t V) { return (int)(((V + 63 + kChunks - 1) / kChunks + kStep - 1) / kStep * kStep); }
+inline int chunks_of(int64_t V) { return (int)((V + 63 + chunk_of(V) - 1) / chunk_of(V)); }
 
-// The workspace: accepted drafts [B], padded to 16 bytes, then the sums of slices [B][slices].
+// The workspace: accepted drafts [B], padded to 16 bytes, then the sums of chunks [B][chunks].
 inline int64_t sums_at(int64_t B) { return (B * 4 + 15) / 16 * 16; }
 
 __device__ __forceinline__ float positive(float x) { return fmaxf(x, 0.f); }  // NaN becomes 0
@@ -63,30 +57,21 @@ __device__ __forceinline__ int accepted_of(const VerifyArgs& a, const Request& x
 // What the token is drawn from: max(p - q, 0), p without the refused draft, or p.
 struct Weights {
   const float *p, *q;
-  int without;
-  __device__ __forceinline__ double at(int j) const {
-    const double x = (double)positive(p[j]);
-    if (q) return fmax(x - (double)positive(q[j]), 0.0);
-    return j == without ? 0.0 : x;
+  int without, V;
+  int before;  // elements from the last whole line's begin to the row's
+  __device__ __forceinline__ double weigh(float x, float y, int j) const {
+    if (j < 0 || j >= V || j == without) return 0.0;
+    return fmax((double)positive(x) - (double)positive(y), 0.0);
   }
 };
 __device__ __forceinline__ Weights weights_of(const VerifyArgs& a, const Request& x, int acc, bool whole) {
   const int64_t row = x.r0 + acc;
   const bool refused = acc < x.n - 1 && !whole;
-  return {a.p + row * a.p_stride, refused && a.q ? a.q + row * a.q_stride : nullptr, refused ? a.tokens[row + 1] : -1};
+  const float* p = a.p + row * a.p_stride;
+  return {p, refused && a.q ? a.q + row * a.q_stride : nullptr, refused && !a.q ? a.tokens[row + 1] : -1, a.V,
+          (int)(reinterpret_cast<uintptr_t>(p) >> 2 & 63)};
 }
 
-// The sum over the workgroup; part: a number a wave.
-__device__ __forceinline__ double group_sum(double s, double* part) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
-  __syncthreads();
-  s = part[0];
-#pragma unroll
-  for (int i = 1; i < kThreads / 64; ++i) s += part[i];
-  return s;
-}
 // The sum over the threads before this one, and over all.
 __device__ __forceinline__ double group_before(double x, double* part, double& all) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -103,7 +88,7 @@ __device__ __forceinline__ double group_before(double x, double* part, double& a
   double base = 0;
   all = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) {
+  for (int i = 0; i < kWaves; ++i) {
     if (i < w) base += part[i];
     all += part[i];
   }
@@ -124,55 +109,71 @@ __device__ __forceinline__ Found group_found(int hit, int last, Found* found) {
   __syncthreads();
   Found f = found[0];
 #pragma unroll
-  for (int i = 1; i < kThreads / 64; ++i) {
+  for (int i = 1; i < kWaves; ++i) {
     f.first = min(f.first, found[i].first);
     f.last = max(f.last, found[i].last);
   }
   return f;
 }
 
-__device__ __forceinline__ double slice_sum(const Weights& w, int j0, int j1) {
+// The sum of a chunk, by one wave; the same in every lane.
+__device__ __forceinline__ double chunk_sum(const Weights& w, int c, int chunk) {
+  const int lane = threadIdx.x & 63, j0 = c * chunk - w.before;
   double s = 0;
-  for (int j = j0 + (int)threadIdx.x; j < j1; j += kStep) {
-    if (j - (int)threadIdx.x + kStep <= j1) {
-      float p[kAhead], q[kAhead];
+  for (int b0 = j0; b0 < min(w.V, j0 + chunk); b0 += kStep) {
+    float p[kAhead], q[kAhead];
+    if (b0 >= 0 && b0 + kStep <= w.V) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) p[i] = w.p[j + kThreads * i];
+      for (int i = 0; i < kAhead; ++i) p[i] = w.p[b0 + 64 * i + lane];
       if (w.q) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) q[i] = w.q[j + kThreads * i];
+        for (int i = 0; i < kAhead; ++i) q[i] = w.q[b0 + 64 * i + lane];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) s += fmax((double)positive(p[i]) - (double)positive(q[i]), 0.0);
       } else {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) s += j + kThreads * i == w.without ? 0.0 : (double)positive(p[i]);
+        for (int i = 0; i < kAhead; ++i) s += b0 + 64 * i + lane == w.without ? 0.0 : (double)positive(p[i]);
       }
     } else {
-      for (int i = j; i < j1; i += kThreads) s += w.at(i);
+      int at[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) at[i] = min(max(b0 + 64 * i + lane, 0), w.V - 1);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) p[i] = w.p[at[i]];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) q[i] = 0.f;
+      if (w.q) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) q[i] = w.q[at[i]];
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) s += w.weigh(p[i], q[i], b0 + 64 * i + lane);
     }
   }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
   return s;
 }
 
-__global__ __launch_bounds__(kThreads) void k_verify_sums(VerifyArgs a, int slice, int32_t* accepted, double* sums) {
-  __shared__ double part[kThreads / 64];
-  const int b = blockIdx.y;
+__global__ __launch_bounds__(kThreads) void k_verify_sums(VerifyArgs a, int chunk, int chunks, int32_t* accepted, double* sums) {
+  const int b = blockIdx.y, lane = threadIdx.x & 63;
   const Request x = request_of(a, b);
   if (x.n == 0) return;
-  const int acc = accepted_of(a, x, threadIdx.x & 63);
-  const int j0 = (int)blockIdx.x * slice, j1 = min(a.V, j0 + slice);
-  const double s = group_sum(slice_sum(weights_of(a, x, acc, false), j0, j1), part);
-  if (threadIdx.x == 0) {
-    sums[(int64_t)b * gridDim.x + blockIdx.x] = s;
-    if (blockIdx.x == 0) accepted[b] = acc;
+  const int acc = accepted_of(a, x, lane);
+  const int c = (int)blockIdx.x * kWaves + (int)(threadIdx.x >> 6);
+  if (c >= chunks) return;
+  const double s = chunk_sum(weights_of(a, x, acc, false), c, chunk);
+  if (lane == 0) {
+    sums[(int64_t)b * chunks + c] = s;
+    if (c == 0) accepted[b] = acc;
   }
 }
 
-__global__ __launch_bounds__(kThreads) void k_verify_draw(VerifyArgs a, int slice, int slices, const int32_t* accepted,
+__global__ __launch_bounds__(kThreads) void k_verify_draw(VerifyArgs a, int chunk, int chunks, const int32_t* accepted,
                                                           const double* sums) {
-  __shared__ double part[kThreads / 64], part2[kThreads / 64], run_of;
-  __shared__ Found found[2][kThreads / 64];
-  __shared__ double row[kBlock + kThreads];  // 17 places for 16: threads side by side use different banks
+  __shared__ double part[kWaves], part2[kWaves], run_of;
+  __shared__ Found found[2][kWaves];
+  __shared__ double again[kChunks];
   const int b = blockIdx.x, i = threadIdx.x;
   if (b == a.B) {  // rows behind the last request
     const int end = min(max(a.cu_q[a.B], 0), a.T);
@@ -190,43 +191,37 @@ __global__ __launch_bounds__(kThreads) void k_verify_draw(VerifyArgs a, int slic
   }
   const int acc = accepted[b];
   const float u = a.sample[b];
-  double mine = i < slices ? sums[(int64_t)b * slices + i] : 0.0, total;
+  double mine = i < chunks ? sums[(int64_t)b * chunks + i] : 0.0, total;
   double before = group_before(mine, part, total);
   const bool whole = !(total > 0);  // nothing is left of p: p itself
   const Weights w = weights_of(a, x, acc, whole);
   if (whole && acc < x.n - 1) {
-    for (int s = 0; s < slices; ++s) {
-      __syncthreads();
-      const double y = group_sum(slice_sum(w, s * slice, min(a.V, (s + 1) * slice)), part);
-      if (i == s) mine = y;
+    for (int c = i / 64; c < chunks; c += kWaves) {
+      const double y = chunk_sum(w, c, chunk);
+      if (i % 64 == 0) again[c] = y;
     }
     __syncthreads();
+    mine = i < chunks ? again[i] : 0.0;
     before = group_before(mine, part, total);
   }
   const double goal = fmin(fmax((double)u, 0.0), 1.0) * total;
   Found f = group_found(mine > 0 && before + mine > goal ? i : kNone, mine > 0 ? i : -1, found[0]);
   int token = -1;
-  const int at = f.first != kNone ? f.first : f.last;  // the slice; -1: no weight anywhere
+  const int at = f.first != kNone ? f.first : f.last;  // the chunk; -1: no weight anywhere
   if (at >= 0) {
     if (i == at) run_of = before;
-    const int end = min(a.V, (at + 1) * slice);
-    for (int b0 = at * slice; b0 < end; b0 += kBlock) {
-      // loaded side by side, taken 16 to a thread
-      double y[kEach];
+    __syncthreads();
+    const int start = at * chunk - w.before, end = min(a.V, start + chunk);
+    for (int b0 = start; b0 < end; b0 += kStep) {
+      const int j = b0 + i * kEach;
+      double y[kEach], s = 0, block;
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
-        const int j = b0 + k * kThreads + i;
-        y[k] = j < end ? w.at(j) : 0.0;
+        const int at = min(max(j + k, 0), a.V - 1);
+        y[k] = w.weigh(w.p[at], w.q ? w.q[at] : 0.f, j + k);
       }
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) row[k * kThreads + i + (k * kThreads + i) / kEach] = y[k];
-      __syncthreads();
-      double s = 0, block;
-#pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        y[k] = row[i * (kEach + 1) + k];
-        s += y[k];
-      }
+      for (int k = 0; k < kEach; ++k) s += y[k];
       const double run = run_of;
       double upto = run + group_before(s, part2, block);
       int hit = kNone, last = -1;
@@ -234,7 +229,7 @@ __global__ __launch_bounds__(kThreads) void k_verify_draw(VerifyArgs a, int slic
       for (int k = 0; k < kEach; ++k) {
         upto += y[k];
         if (y[k] > 0) {
-          last = b0 + i * kEach + k;
+          last = j + k;
           if (upto > goal && hit == kNone) hit = last;
         }
       }
@@ -257,20 +252,19 @@ __global__ __launch_bounds__(kThreads) void k_verify_draw(VerifyArgs a, int slic
 
 }  // namespace
 
-size_t verify_workspace_bytes(int64_t B, int64_t V) { return (size_t)(sums_at(B) + B * slices_of(B, V) * 8); }
+size_t verify_workspace_bytes(int64_t B, int64_t V) { return (size_t)(sums_at(B) + B * chunks_of(V) * 8); }
 
 hipError_t launch_verify(const VerifyArgs& a, void* workspace, hipStream_t st) {
   int32_t* accepted = static_cast<int32_t*>(workspace);
   double* sums = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + sums_at(a.B));
-  int slice = kStep, slices = 0;
+  const int chunk = chunk_of(a.V), chunks = chunks_of(a.V);
   if (a.B > 0) {
-    slice = slice_of(a.B, a.V);
-    slices = slices_of(a.B, a.V);
-    hipLaunchKernelGGL(k_verify_sums, dim3((unsigned)slices, (unsigned)a.B), dim3(kThreads), 0, st, a, slice, accepted, sums);
+    const dim3 grid((unsigned)((chunks + kWaves - 1) / kWaves), (unsigned)a.B);
+    hipLaunchKernelGGL(k_verify_sums, grid, dim3(kThreads), 0, st, a, chunk, chunks, accepted, sums);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(k_verify_draw, dim3((unsigned)a.B + 1), dim3(kThreads), 0, st, a, slice, slices, (const int32_t*)accepted,
+  hipLaunchKernelGGL(k_verify_draw, dim3((unsigned)a.B + 1), dim3(kThreads), 0, st, a, chunk, chunks, (const int32_t*)accepted,
                      (const double*)sums);
   return hipGetLastError();
 }

@@ -782,8 +782,11 @@ def mx_verify_drafts(target_probs, draft_probs, tokens, cu_q, kv_lens, accept_ra
     _meta(cu_q, "cu_q", i32, B + 1)
     _meta(accept_random, "accept_random", f32, T)
     _meta(sample_random, "sample_random", f32, B)
-    if out_tokens is None and accepted is None and new_lens is None:
-        out_tokens, accepted, new_lens = _new((T + 2 * B,), i32, target_probs, stream).split((T, B, B))
+    nbytes = mx_verify_drafts_workspace_bytes(B, V)
+    if workspace is None and nbytes and out_tokens is None and accepted is None and new_lens is None:
+        # one allocation; the workspace first, where torch aligns it
+        words = -(-nbytes // 4)
+        workspace, out_tokens, accepted, new_lens = _new((words + T + 2 * B,), i32, target_probs, stream).split((words, T, B, B))
     else:
         out_tokens = out_tokens if out_tokens is not None else _new((T,), i32, target_probs, stream)
         accepted = accepted if accepted is not None else _new((B,), i32, target_probs, stream)
@@ -791,9 +794,10 @@ def mx_verify_drafts(target_probs, draft_probs, tokens, cu_q, kv_lens, accept_ra
         _meta(out_tokens, "out_tokens", i32, T)
         _meta(accepted, "accepted", i32, B)
         _meta(new_lens, "new_lens", i32, B)
-    nbytes, ws_bytes = mx_verify_drafts_workspace_bytes(B, V), 0
+        if nbytes and workspace is None:
+            workspace = _new((nbytes,), torch.uint8, target_probs, stream)
+    ws_bytes = 0
     if nbytes:
-        workspace = workspace if workspace is not None else _new((nbytes,), torch.uint8, target_probs, stream)
         ws_bytes = _workspace_size(workspace)
     else:
         workspace = None

@@ -309,9 +309,8 @@ enum { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 };
  * Equal c go to the lower expert, equal values to the lower group. c and values are FP64 and are
  * compared to 42 bits (without a bias c is compared by the logits, exactly); weights are formed in
  * FP64 and rounded once. An expert whose logit or bias is -inf or NaN is never chosen and has no part
- * in any sum; +inf counts as the logits'
- * type's largest number. Where fewer than topk experts are left, the rest
- * of the places get id -1 and weight 0, which mx_moe_sort and mx_moe_combine pass over.
+ * in any sum; +inf counts as the logits' type's largest number. Where fewer than topk experts are
+ * left, the rest of the places get id -1 and weight 0; mx_moe_sort gives those no row.
  *  logits: row t's E values of logits_type at element t * logits_stride (any address of that type).
  *  bias: [E] float32, or NULL. num_rows: [1] int32 or NULL: rows from *num_rows on are padding, all
  *  of their places get id -1 and weight 0. topk_ids: [T, topk] int32, topk_weights: [T, topk] float32.
@@ -500,14 +499,15 @@ enum { MX_ROPE_HALVES = 0, MX_ROPE_PAIRS = 1 };
  *    be q_bf16 itself (with the same stride) and must not overlap any input otherwise.
  *  Without queries, q_bf16 NULL and heads_q 0; without keys and values (a layer that reads another's
  *    cache), k_bf16, v_bf16, slots and cache NULL, heads and num_pages 0.
- *  positions: [T] int32; a row whose position is below 0 is padding: nothing of it is read or written.
+ *  positions: [T] int32; a row whose position is below 0 is padding: nothing of it is written or
+ *    reaches a result.
  *  slots: [T] int64; a slot outside [0, num_pages * page_size) writes no key and value (its queries
  *    are still done). Give each slot once.
  *  q_weight, k_weight: [D] float32 or NULL. inv_freq: [rot / 2] float32; NULL with rot 0 for none.
  * Requires 0 <= T <= 2^30, heads and heads_q at most 1024, one of them above 0, D 64, 128 or 256,
  * rot a multiple of 16 in [0, D], eps >= 0 and finite, a finite rope_scale, page_size as above (also
  * without keys). Elements, weights and frequencies must be finite, and so must keys after norm and
- * rotation in FP32. T == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (q, k, v,
+ * rotation in FP32; angles must stay below 2^31. T == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (q, k, v,
  * q_out, cache: 16 bytes; slots: 8; the others 4), MX_ERR_DEVICE, MX_ERR_HIP.
  */
 mx_status mx_kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,

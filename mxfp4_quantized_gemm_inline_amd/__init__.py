@@ -874,12 +874,12 @@ def mx_moe_sort(topk_ids, E: int, first_expert: int = 0, expert_offsets=None, ro
     _meta(topk_ids, "topk_ids", i32)
     T, topk = _dims2(topk_ids, "topk_ids")
     E = int(E)
-    if expert_offsets is None and row_token is None and token_rows is None:
-        # one allocation; each part starts at a multiple of 16 bytes
-        n, m = T * topk, max(E, 0) + 1
-        n4, m4 = (n + 3) // 4 * 4, (m + 3) // 4 * 4
-        whole = _new((m4 + 2 * n4,), i32, topk_ids, stream)
-        expert_offsets, row_token, token_rows = whole[:m], whole[m4:m4 + n], whole[m4 + n4:m4 + n4 + n].view(T, topk)
+    nbytes = mx_moe_sort_workspace_bytes(T, topk, E)
+    if workspace is None and expert_offsets is None and row_token is None and token_rows is None:
+        # one allocation; the workspace first, where torch aligns it
+        sizes = (-(-nbytes // 4), max(E, 0) + 1, T * topk, T * topk)
+        workspace, expert_offsets, row_token, token_rows = _new((sum(sizes),), i32, topk_ids, stream).split(sizes)
+        token_rows = token_rows.view(T, topk)
     else:
         expert_offsets = expert_offsets if expert_offsets is not None else _new((max(E, 0) + 1,), i32, topk_ids, stream)
         row_token = row_token if row_token is not None else _new((T * topk,), i32, topk_ids, stream)
@@ -889,9 +889,10 @@ def mx_moe_sort(topk_ids, E: int, first_expert: int = 0, expert_offsets=None, ro
         _meta(token_rows, "token_rows", i32)
         if token_rows.shape != (T, topk):
             raise ValueError(f"token_rows must have shape {(T, topk)}, got {tuple(token_rows.shape)}")
-    nbytes, ws_bytes = mx_moe_sort_workspace_bytes(T, topk, E), 0
+        if nbytes and workspace is None:
+            workspace = _new((nbytes,), torch.uint8, topk_ids, stream)
+    ws_bytes = 0
     if nbytes:
-        workspace = workspace if workspace is not None else _new((nbytes,), torch.uint8, topk_ids, stream)
         ws_bytes = _workspace_size(workspace)
     else:
         workspace = None

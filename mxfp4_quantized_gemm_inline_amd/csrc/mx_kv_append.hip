@@ -12,6 +12,10 @@ namespace {
 // elements of a row, at the same place in every head that it goes through, so that its weights and angles
 // are one set of registers: with A = weight * cos and B = +-(weight of the other element) * sin an element
 // is r * (x A + other B), r = 1 / sqrt(mean + eps).
+// Bound: HBM. 16411 rows of 32 + 8 heads of 128: 86 us, 4.1 TB/s (floor 72 at a copy's 4.9); the queries
+// alone 58.5 us (4.6 TB/s), keys and values alone 28.5 (FP64 issue; floor 17.4). 101 rows 5.0 us: a
+// launch, positions, angles, heads. Queries in tiles of 16 rows x 256 bytes as keys are: 75 us. All three
+// in one workgroup kind, 16 rows of all heads: 101 us, the registers of keys for all.
 template <int D>
 struct AppendTile {  // of keys and values
   static constexpr int kWidth = D < 128 ? 128 : D;  // elements of a row at a time
@@ -252,7 +256,9 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t field) { return field > 
 
 // Codes of 8 keys, and the scale byte of their block. In FP64, which this chip adds and multiplies as fast
 // as FP32: a key next to a border of the quantizer goes by its exact value, and the cache's bytes do not
-// turn on the order of roundings.
+// turn on the order of roundings. FP32 with a bound on its error, and FP64 only for keys within it of a
+// border, was slower: 30 us against 28 for 16411 rows, and 8 against 4.9 for 101, where some wave has to
+// fetch the seldom path's instructions from memory.
 template <int D, bool kPairs>
 __device__ __forceinline__ uint32_t key_codes(const KvAppendArgs& a, const uint4& k4, const double (&A)[8], const double (&B)[8],
                                               const Place& me, uint32_t& scale) {
@@ -391,7 +397,10 @@ template <int D, bool kPairs>
 hipError_t launch(const KvAppendArgs& a, hipStream_t st) {
   using Tile = AppendTile<D>;
   constexpr int kMost = 1 << 21;  // rows of a launch, which holds fewer than 2^32 threads
-  constexpr int kGroups = 512;    // of queries, and of keys or values, wanted
+  // Workgroups of queries, and of keys or values, wanted: more share out the angles' work less, fewer leave
+  // the chip idle. 512 / 256 / 1024: 1500 rows of 32 + 8 heads 10.4 / 10.3 / 12.6 us, 4000 rows 20.9 / 23.2 / 22.0,
+  // 2051 of 12 + 12 heads of 64 9.0 / 11.1 / 10.1; 500 rows 6.4 / 6.0 / 7.8.
+  constexpr int kGroups = 512;
   for (int64_t first = 0; first < a.T; first += kMost) {
     const int rows = (int)min(a.T - first, (int64_t)kMost);
     AppendGrid g;

@@ -20,6 +20,10 @@ namespace {
 // it is put one to a lane, and each is ranked by comparing it with all of them. Where more than 64 reach
 // the bound (rows of equal logits, the largest all in a few lanes) the largest is taken topk times
 // instead.
+// Bound: instruction issue (the floor of 16411 tokens x 896 bf16 logits is 6.4 us of HBM): 17.7 us, 1.7 TB/s,
+// where the largest taken topk times took 144; 64-bit keys take 24.6 there and 15.7 against 12.9 with 64
+// experts; the bound bisected down to exactly topk lanes 0.7 us more. 256 experts in 8 groups with a
+// bias 4099 tokens 10.0 us. 16 tokens 4.3 us: a launch and the chain of one token.
 
 constexpr int kRouteWaves = 4;
 constexpr int kBisections = 14;  // at most: the lanes that reach the bound may be a quarter more than topk
@@ -369,7 +373,8 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
   RouteShape g = {64, a.E / a.groups};
   while (g.lanes > 64 / a.groups) g.lanes /= 2;
   const int each = (g.size + g.lanes - 1) / g.lanes, fours = (g.size + 4 * g.lanes - 1) / (4 * g.lanes);
-  // four experts in one load where they lie so and it takes no more registers
+  // Four experts in one load where they lie so: 16411 x 896 18.2 us against 25.1 one by one, 256 tokens 5.2
+  // against 6.1; of 64 and 128 experts (one or two a lane) one by one 12.7 against 12.9, 13.2 against 13.5.
   const auto on = [](uint64_t x) { return x % (4 * sizeof(L)) == 0; };
   const bool w4 = g.size % 4 == 0 && on((uint64_t)a.logits) && on((uint64_t)a.stride * sizeof(L)) && each > 2;
   if (w4 && fours <= 4) {
@@ -394,6 +399,11 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
 // workgroup's of the same expert (to token_rows) and counts those, a last one adds where they start; the
 // counts before a workgroup's are summed up there, or, where there are more than kSortSums workgroups,
 // by a launch between the two.
+// Bound: latency, a chain of loads, ballots, LDS counters and barriers a launch, and the launches. 256
+// places of 896 experts 4.8 us; 65536 13.1 (7.0 + 5.6 and the gap; floor 0.2); 524296 16.5 (floor 1.3).
+// kSortAll: 16384 places 9.9 us in one launch against 13.3 in two, 32768 13.2 against 12.2, 65536 19.9
+// against 13.1 (62 where all are one expert's: LDS counters serialize). kSortSums: 131072 places (64
+// workgroups) 15.1 us summed up there, 15.8 with the launch between; 160000 18.8 against 16.4.
 
 constexpr int kSortAll = 16384;
 constexpr int kSortChunk = 2048;   // places of a workgroup of the others, or a multiple
@@ -452,11 +462,8 @@ __device__ __forceinline__ void next_places(int (&at)[K], const int (&e)[K], int
   for (int i = 0; i < K; ++i) at[i] = e[i] >= 0 ? __shfl(base[i], leader[i]) + at[i] : -1;
 }
 
-// W waves a workgroup, kSteps times 64 places a wave.
-template <int W, int kSteps>
-__global__ __launch_bounds__(64 * W) void k_moe_sort(SortArgs a) {
-  constexpr int kThreads = 64 * W, kExperts = 1024 / kThreads;  // experts a thread
-  constexpr int each = 64 * kSteps, share = W * each;
+__global__ __launch_bounds__(1024) void k_moe_sort(SortArgs a) {
+  constexpr int W = 16, kThreads = 64 * W, kSteps = 2, each = 64 * kSteps, share = W * each;  // places of a wave, of a workgroup
   __shared__ int32_t cnt[W][1024];
   __shared__ int32_t before[1024], behind[1024];
   __shared__ int32_t part[W];
@@ -482,38 +489,28 @@ __global__ __launch_bounds__(64 * W) void k_moe_sort(SortArgs a) {
     }
   }
   __syncthreads();
-  int x[kExperts], sum = 0;
+  const int e = threadIdx.x;  // an expert a thread
+  int all = 0;
+  if (e < a.E) {
+    all = before[e] + behind[e];
 #pragma unroll
-  for (int i = 0; i < kExperts; ++i) {
-    const int e = (int)threadIdx.x * kExperts + i;
-    x[i] = 0;
-    if (e < a.E) {
-      x[i] = before[e] + behind[e];
-#pragma unroll
-      for (int j = 0; j < W; ++j) x[i] += cnt[j][e];
-    }
-    sum += x[i];
+    for (int j = 0; j < W; ++j) all += cnt[j][e];
   }
-  int run = group_scan<W>(sum, part) - sum;
+  const int run = group_scan<W>(all, part) - all;
+  if (e < a.E) {
+    if (blockIdx.x == 0) a.offsets[e] = run;
+    int base = run + before[e];
 #pragma unroll
-  for (int i = 0; i < kExperts; ++i) {
-    const int e = (int)threadIdx.x * kExperts + i;
-    if (e < a.E) {
-      if (blockIdx.x == 0) a.offsets[e] = run;
-      int base = run + before[e];
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        const int c = cnt[j][e];
-        cnt[j][e] = base;
-        base += c;
-      }
+    for (int j = 0; j < W; ++j) {
+      const int c = cnt[j][e];
+      cnt[j][e] = base;
+      base += c;
     }
-    run += x[i];
   }
   int R = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) R += part[i];
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = R;
+  if (blockIdx.x == 0 && e == 0) a.offsets[a.E] = R;
   __syncthreads();
   int own[kSteps], at[kSteps];
   const int m0 = n0 + w * each + (int)(threadIdx.x & 63);
@@ -636,12 +633,8 @@ size_t moe_sort_workspace_bytes(int64_t N, int64_t E) {
 }
 
 hipError_t launch_moe_sort(const SortArgs& a, void* workspace, hipStream_t st) {
-  if (a.N <= 1024) {
-    hipLaunchKernelGGL((k_moe_sort<4, 4>), dim3(1), dim3(256), 0, st, a);
-    return hipGetLastError();
-  }
   if (a.N <= kSortAll) {
-    hipLaunchKernelGGL((k_moe_sort<16, 2>), dim3((unsigned)((a.N + 2047) / 2048)), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL(k_moe_sort, dim3((unsigned)max((a.N + 2047) / 2048, 1)), dim3(1024), 0, st, a);
     return hipGetLastError();
   }
   const int chunk = sort_chunk(a.N), chunks = sort_chunks(a.N);

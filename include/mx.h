@@ -537,7 +537,7 @@ mx_status mx_kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16,
  *  out_tokens: [T] int32: at a request's rows its accepted drafts, then the drawn token (-1 where p is
  *    0 everywhere), then -1; -1 from row cu_q[B] on.
  *  accepted: [B] int32, how many drafts. new_lens: [B] int32, kv_lens[b] less the refused drafts (kv_lens
- *    itself may be given).
+ *    itself may be given; no other output may overlap an input).
  *  A request without rows has 0 accepted and keeps its length.
  * workspace: mx_verify_drafts_workspace_bytes(B, V) bytes, 16-byte aligned. Requires 0 <= T <= 2^30,
  * 0 <= B <= 2^16 - 2, 1 <= V <= 2^24, strides in [V, 2^32) (or 0). Errors: MX_ERR_NULL, MX_ERR_SHAPE,

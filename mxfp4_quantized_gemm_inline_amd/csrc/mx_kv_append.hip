@@ -76,15 +76,23 @@ __device__ __forceinline__ double exact_norm(const float (&x)[8], float eps) {
   return rsqrt(fmax(sum_squares<D, double>(x) * (1.0 / D) + (double)eps, 0x1p-126));
 }
 // The same in FP32, off by at most 10 u (u = 2^-24: half of the sum's 8 + 5 roundings, the product, the
-// sum with eps, the root's step); in FP64 where a square would leave FP32's range.
+// sum with eps, the root's step); in FP64 where a square would leave FP32's range. y: what is multiplied
+// with it, turned from x, which is formed again of 2^-64 x, for 2^64 times the norm, where x is so large
+// that weight or scale could take it out of range, or the norm is subnormal.
 template <int D>
-__device__ __forceinline__ float fast_norm(const float (&x)[8], float eps) {
+__device__ __forceinline__ float fast_norm(const float (&x)[8], float eps, float (&y)[8], const float (&o)[8], const float (&A)[8],
+                                           const float (&B)[8]) {
   const float s = sum_squares<D, float>(x);
   float n = __builtin_amdgcn_rsqf(fmaf(s, 1.f / D, eps));
   const bool inside = s > 1e-30f && s < 1e38f;
   if (__any(!inside)) {  // all lanes, as they sum together
-    const float m = (float)exact_norm<D>(x, eps);
-    if (!inside) n = m;
+    const double m = exact_norm<D>(x, eps);
+    if (!inside) n = (float)m;
+    if (!(s < 1e38f)) {
+      n = (float)(m * 0x1p64);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i] * 0x1p-64f, A[i], o[i] * 0x1p-64f * B[i]);
+    }
   }
   return n;
 }
@@ -231,7 +239,7 @@ __device__ __forceinline__ void append_queries(const KvAppendArgs& a, Shared& sh
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], A[i], o[i] * B[i]);
     if (a.q_weight) {
-      const float n = fast_norm<D>(x, a.eps);
+      const float n = fast_norm<D>(x, a.eps, y, o, A, B);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] *= n;
     }

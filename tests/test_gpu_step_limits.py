@@ -11,7 +11,7 @@ from oracle import mx_oracle as O
 from oracle import mx_step_oracle as S
 
 from gpu_util import dev_bf16, host_bits, lib_or_fail, torch_or_skip
-from test_gpu_step import _check_route, _check_sort, _check_verify, _logits, _verify_inputs, dev
+from test_gpu_step import _check_append, _check_route, _check_sort, _check_verify, _logits, _verify_inputs, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -160,6 +160,16 @@ def test_append_leaves_what_lies_beside_its_rows(T, Hq, H, D):
     q2 = mx.mx_kv_append(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], pos, slots, b, 16, **kw)
     assert torch.equal(q1, q2) and torch.equal(a, b)
     assert bool((out[:, 0] == 3).all()) and bool((out[:, -1] == 3).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_norms_of_heads_near_the_largest(D):
+    """What weight and scale alone would take past FP32's range, and norms below its normal numbers."""
+    torch_or_skip()
+    mx = lib_or_fail()
+    for pairs in (False, True):
+        _check_append(mx, 20, 3, 2, D, 16, std=6e37, eps=0.0, rope_scale=8.0, pairs=pairs)
+        _check_append(mx, 20, 3, 2, D, 16, std=6e37, eps=1e-6, rope_scale=8.0, pairs=pairs, rot=D // 2, seed=1)
 
 
 def test_append_of_zero_heads_without_eps():

@@ -786,7 +786,7 @@ def mx_verify_drafts(target_probs, draft_probs, tokens, cu_q, kv_lens, accept_ra
     if workspace is None and nbytes and out_tokens is None and accepted is None and new_lens is None:
         # one allocation; the workspace first, where torch aligns it
         words = -(-nbytes // 4)
-        workspace, out_tokens, accepted, new_lens = _new((words + T + 2 * B,), i32, target_probs, stream).split((words, T, B, B))
+        workspace, out_tokens, accepted, new_lens = _new((words + T + 2 * B,), i32, target_probs, stream).split_with_sizes((words, T, B, B))
     else:
         out_tokens = out_tokens if out_tokens is not None else _new((T,), i32, target_probs, stream)
         accepted = accepted if accepted is not None else _new((B,), i32, target_probs, stream)
@@ -878,7 +878,7 @@ def mx_moe_sort(topk_ids, E: int, first_expert: int = 0, expert_offsets=None, ro
     if workspace is None and expert_offsets is None and row_token is None and token_rows is None:
         # one allocation; the workspace first, where torch aligns it
         sizes = (-(-nbytes // 4), max(E, 0) + 1, T * topk, T * topk)
-        workspace, expert_offsets, row_token, token_rows = _new((sum(sizes),), i32, topk_ids, stream).split(sizes)
+        workspace, expert_offsets, row_token, token_rows = _new((sum(sizes),), i32, topk_ids, stream).split_with_sizes(sizes)
         token_rows = token_rows.view(T, topk)
     else:
         expert_offsets = expert_offsets if expert_offsets is not None else _new((max(E, 0) + 1,), i32, topk_ids, stream)

@@ -400,16 +400,20 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
 // counts before a workgroup's are summed up there, or, where there are more than kSortSums workgroups,
 // by a launch between the two.
 // Bound: latency, a chain of loads, ballots, LDS counters and barriers a launch, and the launches. 256
-// places of 896 experts 4.8 us; 65536 13.1 (7.0 + 5.6 and the gap; floor 0.2); 524296 16.5 (floor 1.3).
-// kSortAll: 16384 places 9.9 us in one launch against 13.3 in two, 32768 13.2 against 12.2, 65536 19.9
-// against 13.1 (62 where all are one expert's: LDS counters serialize). kSortSums: 131072 places (64
-// workgroups) 15.1 us summed up there, 15.8 with the launch between; 160000 18.8 against 16.4.
+// places of 896 experts 4.8 us; 65536 11.7 (5.8 + 5.6 and the gap; floor 0.2); 524296 16.0 (floor 1.3);
+// 1600000 40 (15 + 4 + 18; floor 4: the rows' scattered words).
+// kSortAll: 16384 places 9.9 us in one launch against 12.0 in two, 32768 13.1 against 10.8, 65536 19.9
+// against 11.7 (62 where all are one expert's: LDS counters serialize). kSortSums: 131072 places (64
+// workgroups) 13.7 us summed up there, 14.5 with the launch between; 160000 17.5 against 15.2.
 
 constexpr int kSortAll = 16384;
 constexpr int kSortChunk = 2048;   // places of a workgroup of the others, or a multiple
-constexpr int kSortChunks = 1024;  // workgroups of those, at most
+constexpr int kSortChunks = 512;   // workgroups of those, at most. 512 / 1024 / 256: 1600000 places 40.3 / 43.5 / 40.8 us, 524296 16.0 / 16.0 / 18.2
 constexpr int kSortSums = 64;
-constexpr int kEach = 8;           // places that a lane loads ahead
+constexpr int kEach = 8;           // places that a lane loads ahead in the one launch
+// Waves of a workgroup that ranks, and places a lane. 8 / 4 / 16 waves: 65536 places 11.8 / 13.1 / 11.5 us,
+// 320000 17.6 / 18.9 / 17.8, 1600000 43.9 / 45.3 / 46.9.
+constexpr int kRankWaves = 8, kRankEach = kSortChunk / 64 / kRankWaves;
 inline int sort_chunk(int64_t N) {
   const int64_t each = (N + kSortChunks - 1) / kSortChunks;
   return (int)((max(each, (int64_t)kSortChunk) + kSortChunk - 1) / kSortChunk * kSortChunk);
@@ -529,27 +533,27 @@ __global__ __launch_bounds__(1024) void k_moe_sort(SortArgs a) {
 // token_rows: each place's number among this workgroup's of its expert; counts: how many of each,
 // [chunks][E], or with kScan [E][chunks].
 template <bool kScan>
-__global__ __launch_bounds__(256) void k_moe_sort_rank(SortArgs a, int chunk, int32_t* counts) {
-  __shared__ int32_t cnt[4][1024];
+__global__ __launch_bounds__(64 * kRankWaves) void k_moe_sort_rank(SortArgs a, int chunk, int32_t* counts) {
+  __shared__ int32_t cnt[kRankWaves][1024];
   __shared__ int32_t sums[1024];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < a.E; e += 256) sums[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += 64 * kRankWaves) sums[e] = 0;
   const int64_t n0 = (int64_t)blockIdx.x * chunk, n1 = min((int64_t)a.N, n0 + chunk);
   for (int64_t s0 = n0; s0 < n1; s0 += kSortChunk) {
-    int e[kEach], at[kEach];
+    int e[kRankEach], at[kRankEach];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int64_t n = s0 + (w * kEach + i) * 64 + lane;
+    for (int i = 0; i < kRankEach; ++i) {
+      const int64_t n = s0 + (w * kRankEach + i) * 64 + lane;
       e[i] = n < n1 ? local_expert(a, (int)n) : -1;
     }
     for (int i = lane; i < a.E; i += 64) cnt[w][i] = 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are in order
     next_places(at, e, a.bits, cnt[w]);
     __syncthreads();
-    for (int i = threadIdx.x; i < a.E; i += 256) {
+    for (int i = threadIdx.x; i < a.E; i += 64 * kRankWaves) {
       int base = sums[i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kRankWaves; ++j) {
         const int c = cnt[j][i];
         cnt[j][i] = base;
         base += c;
@@ -558,12 +562,12 @@ __global__ __launch_bounds__(256) void k_moe_sort_rank(SortArgs a, int chunk, in
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int64_t n = s0 + (w * kEach + i) * 64 + lane;
+    for (int i = 0; i < kRankEach; ++i) {
+      const int64_t n = s0 + (w * kRankEach + i) * 64 + lane;
       if (n < n1) a.token_rows[n] = e[i] >= 0 ? cnt[w][e[i]] + at[i] : -1;
     }
   }
-  for (int e = threadIdx.x; e < a.E; e += 256) counts[kScan ? (int64_t)e * gridDim.x + blockIdx.x : (int64_t)blockIdx.x * a.E + e] = sums[e];
+  for (int e = threadIdx.x; e < a.E; e += 64 * kRankWaves) counts[kScan ? (int64_t)e * gridDim.x + blockIdx.x : (int64_t)blockIdx.x * a.E + e] = sums[e];
 }
 
 // A wave per expert: counts become the sums before them, totals: [E] their sums.
@@ -640,7 +644,7 @@ hipError_t launch_moe_sort(const SortArgs& a, void* workspace, hipStream_t st) {
   const int chunk = sort_chunk(a.N), chunks = sort_chunks(a.N);
   int32_t* totals = static_cast<int32_t*>(workspace);
   int32_t* counts = totals + a.E;
-  const dim3 grid((unsigned)chunks), block(256);
+  const dim3 grid((unsigned)chunks), block(64 * kRankWaves);
   const bool scan = chunks > kSortSums;
   if (scan) hipLaunchKernelGGL(k_moe_sort_rank<true>, grid, block, 0, st, a, chunk, counts);
   else hipLaunchKernelGGL(k_moe_sort_rank<false>, grid, block, 0, st, a, chunk, counts);

@@ -360,8 +360,9 @@ hipError_t route(const RouteArgs& a, const RouteShape& g, hipStream_t st) {
   constexpr int kMost = 1 << 22;  // rows of a launch, which holds fewer than 2^32 threads
   for (int64_t first = 0; first < a.T; first += kMost) {
     const dim3 grid((unsigned)((min(a.T - first, (int64_t)kMost) + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
-    if (a.groups > 1) hipLaunchKernelGGL((k_moe_route<Key, L, V, W, true>), grid, block, 0, st, a, g, (int)first);
-    else hipLaunchKernelGGL((k_moe_route<Key, L, V, W, false>), grid, block, 0, st, a, g, (int)first);
+    // 32 experts a lane only where groups, no power of two of them, leave lanes over
+    if (V == 32 || a.groups > 1) hipLaunchKernelGGL((k_moe_route<Key, L, V, W, true>), grid, block, 0, st, a, g, (int)first);
+    else if constexpr (V < 32) hipLaunchKernelGGL((k_moe_route<Key, L, V, W, false>), grid, block, 0, st, a, g, (int)first);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -374,13 +375,15 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
   while (g.lanes > 64 / a.groups) g.lanes /= 2;
   const int each = (g.size + g.lanes - 1) / g.lanes, fours = (g.size + 4 * g.lanes - 1) / (4 * g.lanes);
   // Four experts in one load where they lie so: 16411 x 896 18.2 us against 25.1 one by one, 256 tokens 5.2
-  // against 6.1; of 64 and 128 experts (one or two a lane) one by one 12.7 against 12.9, 13.2 against 13.5.
+  // against 6.1; 1000 experts in 5 groups 35 against 47, with a bias 125 against 148; of 64 and 128 experts (one
+  // or two a lane) one by one 12.7 against 12.9, 13.2 against 13.5.
   const auto on = [](uint64_t x) { return x % (4 * sizeof(L)) == 0; };
   const bool w4 = g.size % 4 == 0 && on((uint64_t)a.logits) && on((uint64_t)a.stride * sizeof(L)) && each > 2;
-  if (w4 && fours <= 4) {
+  if (w4) {
     if (fours == 1) return route<Key, L, 4, 4>(a, g, st);
     if (fours == 2) return route<Key, L, 8, 4>(a, g, st);
-    return route<Key, L, 16, 4>(a, g, st);
+    if (fours <= 4) return route<Key, L, 16, 4>(a, g, st);
+    return route<Key, L, 32, 4>(a, g, st);
   }
   if (each == 1) return route<Key, L, 1, 1>(a, g, st);
   if (each == 2) return route<Key, L, 2, 1>(a, g, st);

@@ -16,7 +16,7 @@ from test_gpu_step import _check_append, _check_route, _check_sort, _check_verif
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("E,groups,keep", [(896, 1, 1), (256, 8, 3), (1000, 5, 2), (64, 1, 1), (1024, 1, 1)])
+@pytest.mark.parametrize("E,groups,keep", [(896, 1, 1), (256, 8, 3), (1000, 5, 2), (1005, 5, 2), (64, 1, 1), (1024, 1, 1)])
 @pytest.mark.parametrize("f32", [False, True])
 def test_route_where_the_largest_lie_together(E, groups, keep, f32):
     """The topk largest next to each other, at strides of a lane's share, one of them far above, rising and
@@ -70,7 +70,7 @@ def test_route_past_32_bit_offsets():
 
 
 @pytest.mark.parametrize("T,topk,E", [(1023, 1, 7), (1024, 1, 1024), (1025, 1, 3), (2047, 8, 896), (2048, 8, 896), (2049, 8, 896), (16384, 1, 5), (16385, 1, 5),
-                                      (8192, 16, 64), (8193, 16, 64), (131072, 1, 1), (131073, 1, 1), (262145, 8, 1024)])
+                                      (8192, 16, 64), (8193, 16, 64), (131072, 1, 1), (131073, 1, 1), (1 << 20, 1, 300), ((1 << 20) + 1, 1, 300), (262145, 8, 1024)])
 def test_sort_at_the_borders_of_its_paths(T, topk, E):
     torch_or_skip()
     mx = lib_or_fail()

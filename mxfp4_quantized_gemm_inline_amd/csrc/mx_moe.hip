@@ -21,12 +21,16 @@ namespace {
 // the bound (rows of equal logits, the largest all in a few lanes) the largest is taken topk times
 // instead.
 // Bound: instruction issue (the floor of 16411 tokens x 896 bf16 logits is 6.4 us of HBM): 17.7 us, 1.7 TB/s,
-// where the largest taken topk times took 144; 64-bit keys take 24.6 there and 15.7 against 12.9 with 64
-// experts; the bound bisected down to exactly topk lanes 0.7 us more. 256 experts in 8 groups with a
-// bias 4099 tokens 10.0 us. 16 tokens 4.3 us: a launch and the chain of one token.
+// where the largest taken topk times took 144; 64-bit keys take 24.6 there; the bound bisected
+// down to exactly topk lanes 0.7 us more. 64 experts 8.9 us. 256 experts in 8 groups with a bias 4099 tokens
+// 10.3 us. 16 tokens 4.3 us: a launch and the chain of one token.
 
 constexpr int kRouteWaves = 4;
-constexpr int kBisections = 14;  // at most: the lanes that reach the bound may be a quarter more than topk
+constexpr int kList = 64;        // keys that are ranked, at most
+// At most: the lanes that reach the bound may be a quarter more than topk, or as many as have kList keys
+// together. A quarter alone: 64, 128, 256 experts, topk 6 to 8, 16411 tokens 12.8, 13.3, 13.7 us against 8.9,
+// 11.5, 12.7; no bound for one key a lane, longer lists, 10.0 against 8.9.
+constexpr int kBisections = 14;
 
 template <int kControl, int kRows = 0xF>
 __device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
@@ -167,7 +171,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
   typedef typename Key::T T;
   constexpr bool k64 = sizeof(T) == 8;
   constexpr float kLargest = sizeof(L) == 2 ? 0x1.FEp127f : 0x1.FFFFFEp127f;  // the logits' type's
-  __shared__ __attribute__((aligned(16))) T found[kRouteWaves][64];
+  __shared__ __attribute__((aligned(16))) T found[kRouteWaves][kList];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int rows = a.num_rows ? min(*a.num_rows, a.T) : a.T;
   const int lanes = kGroups ? g.lanes : 64, size = kGroups ? g.size : a.E, groups = kGroups ? a.groups : 1;
@@ -287,6 +291,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
   const uint32_t c = Key::coarse(mine);
   uint32_t lo = 0, hi = wave_max(c);
   lo = ~wave_max(~c);
+  const int most = max(a.topk + a.topk / 4, kList / V);
   for (int i = 0; i < kBisections && lo < hi; ++i) {
     const uint32_t mid = lo + (hi - lo + 1) / 2;
     const int n = (int)__popcll(__ballot(c >= mid));
@@ -294,7 +299,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
       hi = mid - 1;
     } else {
       lo = mid;
-      if (n <= a.topk + a.topk / 4) break;
+      if (n <= most) break;
     }
   }
   const T bound = Key::larger(Key::reaching(lo), Key::kLeast);
@@ -305,7 +310,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
   const int upto = (int)wave_scan((uint32_t)mine_n), n = (int)lane_value((uint32_t)upto, 63);
   T chosen = Key::kNone;
   int rank = lane;
-  if (n <= 64) {
+  if (n <= kList) {
     found[w][lane] = Key::kNone;
     int at = upto - mine_n;
 #pragma unroll
@@ -375,8 +380,8 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
   while (g.lanes > 64 / a.groups) g.lanes /= 2;
   const int each = (g.size + g.lanes - 1) / g.lanes, fours = (g.size + 4 * g.lanes - 1) / (4 * g.lanes);
   // Four experts in one load where they lie so: 16411 x 896 18.2 us against 25.1 one by one, 256 tokens 5.2
-  // against 6.1; 1000 experts in 5 groups 35 against 47, with a bias 125 against 148; of 64 and 128 experts (one
-  // or two a lane) one by one 12.7 against 12.9, 13.2 against 13.5.
+  // against 6.1; 1000 experts in 5 groups 35 against 47, with a bias 125 against 148. Of 64 and 128 experts
+  // (one or two a lane) one by one 8.9 against 10.1, 11.6 against 12.4.
   const auto on = [](uint64_t x) { return x % (4 * sizeof(L)) == 0; };
   const bool w4 = g.size % 4 == 0 && on((uint64_t)a.logits) && on((uint64_t)a.stride * sizeof(L)) && each > 2;
   if (w4) {

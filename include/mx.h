@@ -307,8 +307,8 @@ enum { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 };
  *   topk_weights[t][i] = scale * s[id], with renormalize != 0 over the sum of s over the chosen (0
  *     where that sum is 0).
  * Equal c go to the lower expert, equal values to the lower group. c and values are FP64 and are
- * compared to 42 bits (without a bias c is compared by the logits, exactly); weights are formed in
- * FP64 and rounded once. An expert whose logit or bias is -inf or NaN is never chosen and has no part
+ * compared to 42 bits, to which c is cut and a value, the sum of c as they are, rounded (without a
+ * bias c is compared by the logits, exactly); weights are formed in FP64 and rounded once. An expert whose logit or bias is -inf or NaN is never chosen and has no part
  * in any sum; +inf counts as the logits' type's largest number. Where fewer than topk experts are
  * left, the rest of the places get id -1 and weight 0; mx_moe_sort gives those no row.
  *  logits: row t's E values of logits_type at element t * logits_stride (any address of that type).

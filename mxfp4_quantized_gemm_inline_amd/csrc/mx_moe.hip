@@ -133,6 +133,11 @@ struct Key64 {
   static __device__ __forceinline__ double value(T k) {
     return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~1023ull);
   }
+  // Rounded to the bits that keys hold. Sums are, where logits and biases that give equal ones in exact
+  // arithmetic (sigmoids of x and -x, a bias on the one or the other) may differ by an FP64 rounding.
+  static __device__ __forceinline__ double rounded(double c) {
+    return __builtin_bit_cast(double, (__builtin_bit_cast(uint64_t, c) + 512) & ~1023ull);
+  }
   static __device__ __forceinline__ float logit(T k) { return (float)value(k); }
   static __device__ __forceinline__ T larger(T a, T b) { return fmax(a, b); }
   static __device__ __forceinline__ uint32_t coarse(T k) { return in_order((uint32_t)(__builtin_bit_cast(uint64_t, k) >> 32)); }
@@ -246,10 +251,14 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] /= sum;
   }
+  if (kGroups && k64 && a.bias) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] += (double)bias[v];
+  }
   T key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if constexpr (k64) key[v] = Key::of(a.bias ? p[v] + (double)bias[v] : (double)fminf(x[v], kLargest), number(v));
+    if constexpr (k64) key[v] = Key::of(!a.bias ? (double)fminf(x[v], kLargest) : kGroups ? p[v] : p[v] + (double)bias[v], number(v));
     else key[v] = Key::of(fminf(x[v], kLargest), number(v));
     if (masked(v)) key[v] = Key::kNone;
   }
@@ -260,7 +269,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
       double one = Key64::kNone, two = Key64::kNone;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const double y = masked(v) ? Key64::kNone : a.bias || a.group_top == 1 ? Key64::value(key[v]) : p[v];
+        // scores or c as they are: of two c that cancel nothing may be left of their keys' 42 bits
+        const double y = masked(v) ? Key64::kNone : scored ? p[v] : Key64::value(key[v]);
         two = fmax(two, fmin(one, y));
         one = fmax(one, y);
       }
@@ -270,7 +280,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
         one = fmax(one, y);
       }
       if (a.group_top == 2 && two > Key64::kNone) one += two;
-      if (one > Key64::kNone) best = Key64::of(one, my_group);
+      if (one > Key64::kNone) best = Key64::of(Key64::rounded(one), my_group);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) best = max(best, key[v]);

@@ -26,6 +26,12 @@ def truncated(x: np.ndarray) -> np.ndarray:
     return (x.view(np.uint64) & ~np.uint64(1023)).view(np.float64)
 
 
+def rounded(x: float) -> float:
+    """A group's value as it is compared: rounded to those bits, halves away from 0."""
+    x = np.clip(np.array([x], dtype=np.float64), -1e300, 1e300)
+    return float(truncated((x.view(np.uint64) + np.uint64(512)).view(np.float64))[0])
+
+
 def route(logits, topk, bias=None, sigmoid=False, groups=1, topk_groups=1, group_top=2, renormalize=True, scale=1.0, rows=None,
           largest=FLT_MAX):
     """(ids int32 [T, topk], weights float64 [T, topk]) token by token; logits are float32 values of a type
@@ -47,8 +53,9 @@ def route(logits, topk, bias=None, sigmoid=False, groups=1, topk_groups=1, group
             else:
                 s = np.where(ok, np.exp(l - l[ok].max()), 0.0)
                 s = s / s.sum()
-            c = truncated(l if bias is None else s + np.asarray(bias, dtype=np.float64))
-            by = s if bias is None and group_top == 2 else c
+            full = l if bias is None else s + np.asarray(bias, dtype=np.float64)
+            c = truncated(full)
+            by = s if bias is None and group_top == 2 else full
         left = [e for e in range(E) if ok[e]]
         if groups > 1:
             n = E // groups
@@ -56,7 +63,7 @@ def route(logits, topk, bias=None, sigmoid=False, groups=1, topk_groups=1, group
             for g in range(groups):
                 best = sorted((by[e] for e in range(g * n, g * n + n) if ok[e]), reverse=True)[:group_top]
                 if best:
-                    value[g] = truncated(best[0] + best[1] if len(best) > 1 else best[0])
+                    value[g] = rounded(best[0] + best[1] if len(best) > 1 else best[0])
             keep = sorted(value, key=lambda g: (-value[g], g))[:topk_groups]
             left = [e for e in left if e // n in keep]
         chosen = sorted(left, key=lambda e: (-c[e], e))[:topk]

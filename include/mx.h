@@ -491,8 +491,8 @@ enum { MX_ROPE_HALVES = 0, MX_ROPE_PAIRS = 1 };
  *   element pairs (a, b) of the first `rot` elements, number i of rot / 2 of them, become
  *   (a cos - b sin, a sin + b cos) with the angle positions[t] * inv_freq[i], formed in FP64, and cos
  *   and sin times rope_scale.
- * Queries are worked out in FP32 (the angles and norms past its range in FP64) and rounded once to
- * bf16, to q_out. Keys are quantized as FP64 arithmetic, rounded to FP32, has them, values as they are,
+ * Queries are worked out in FP32 (angles, and heads and weights past its range, in FP64) and rounded
+ * once to bf16, to q_out. Keys are quantized as FP64 arithmetic, rounded to FP32, has them, values as they are,
  * both with the rule at the top of this file into slot slots[t] of the cache, as mx_kv_write does.
  *  q_bf16, k_bf16, v_bf16: row t's heads_q * D (heads * D) values at element t * q_stride (k_stride,
  *    v_stride); q_out likewise with q_out_stride >= heads_q * D. Strides are multiples of 8. q_out may
@@ -506,9 +506,10 @@ enum { MX_ROPE_HALVES = 0, MX_ROPE_PAIRS = 1 };
  *  q_weight, k_weight: [D] float32 or NULL. inv_freq: [rot / 2] float32; NULL with rot 0 for none.
  * Requires 0 <= T <= 2^30, heads and heads_q at most 1024, one of them above 0, D 64, 128 or 256,
  * rot a multiple of 16 in [0, D], eps >= 0 and finite, a finite rope_scale, page_size as above (also
- * without keys). Elements, weights and frequencies must be finite, and so must keys after norm and
- * rotation in FP32; angles must stay below 2^31. T == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (q, k, v,
- * q_out, cache: 16 bytes; slots: 8; the others 4), MX_ERR_DEVICE, MX_ERR_HIP.
+ * without keys). Elements, weights, frequencies and weights times rope_scale must be finite in FP32, and
+ * so must keys after norm and rotation and, where q_weight is NULL, each a cos and b sin of the queries
+ * (times rope_scale); angles must stay below 2^31. T == 0 is a no-op. Errors: MX_ERR_NULL, MX_ERR_SHAPE,
+ * MX_ERR_ALIGN (q, k, v, q_out, cache: 16 bytes; slots: 8; the others 4), MX_ERR_DEVICE, MX_ERR_HIP.
  */
 mx_status mx_kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,
                        const void* v_bf16, int64_t v_stride, const int32_t* positions, const int64_t* slots,

@@ -75,26 +75,28 @@ template <int D>
 __device__ __forceinline__ double exact_norm(const float (&x)[8], float eps) {
   return rsqrt(fmax(sum_squares<D, double>(x) * (1.0 / D) + (double)eps, 0x1p-126));
 }
-// The same in FP32, off by at most 10 u (u = 2^-24: half of the sum's 8 + 5 roundings, the product, the
-// sum with eps, the root's step); in FP64 where a square would leave FP32's range. y: what is multiplied
-// with it, turned from x, which is formed again of 2^-64 x, for 2^64 times the norm, where x is so large
-// that weight or scale could take it out of range, or the norm is subnormal.
+// Normed and turned queries, y = (x A + o B) n, in FP32 where nothing on the way can leave its range. The norm is
+// then off by at most 10 u (u = 2^-24: half of the sum's 8 + 5 roundings, the product, the sum with eps,
+// the root's step). Below: with mean + eps of kLeastMean n is 2^14 at most, and what products below the normal
+// numbers lose, 2^-150 each, is less than bf16 holds. Above: sums of squares under 1e38 and coefficients
+// of up to kWide (wide: some are larger) give terms under 2^124. All else is FP64's: heads whose root mean square is
+// below 6e-5 where eps is below 4e-9, or above 1e18, and weights or scales of more than 1e18.
+constexpr float kLeastMean = 0x1p-28f, kWide = 0x1p60f;
 template <int D>
-__device__ __forceinline__ float fast_norm(const float (&x)[8], float eps, float (&y)[8], const float (&o)[8], const float (&A)[8],
-                                           const float (&B)[8]) {
-  const float s = sum_squares<D, float>(x);
-  float n = __builtin_amdgcn_rsqf(fmaf(s, 1.f / D, eps));
-  const bool inside = s > 1e-30f && s < 1e38f;
+__device__ __forceinline__ void normed(float (&y)[8], const float (&x)[8], const float (&o)[8], const float (&A)[8], const float (&B)[8],
+                                       float eps, bool wide) {
+  const float s = sum_squares<D, float>(x), mean = fmaf(s, 1.f / D, eps), n = __builtin_amdgcn_rsqf(mean);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], A[i], o[i] * B[i]) * n;
+  const bool inside = mean >= kLeastMean && s < 1e38f && !wide;
   if (__any(!inside)) {  // all lanes, as they sum together
     const double m = exact_norm<D>(x, eps);
-    if (!inside) n = (float)m;
-    if (!(s < 1e38f)) {
-      n = (float)(m * 0x1p64);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i] * 0x1p-64f, A[i], o[i] * 0x1p-64f * B[i]);
+    for (int i = 0; i < 8; ++i) {
+      const float z = (float)(fma((double)x[i], (double)A[i], (double)o[i] * (double)B[i]) * m);
+      if (!inside) y[i] = z;
     }
   }
-  return n;
 }
 
 // cos and sin of pos * freq. The product is formed in FP64 and that number is the angle: it is reduced
@@ -230,18 +232,21 @@ __device__ __forceinline__ void append_queries(const KvAppendArgs& a, Shared& sh
   const Place me = place_of<D, kPairs>(lane, pos, a.rot);
   float A[8], B[8];
   coefficients<D, kPairs, float>(A, B, a, sh.turn + w * (D / 2), lane, 64, a.q_weight, me);
+  float largest = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) largest = fmaxf(largest, fmaxf(fabsf(A[i]), fabsf(B[i])));
+  const bool wide = largest > kWide;
   for (; e < a.Hq * D; e += step * kQueryWidth) {
     const uint4 x4 = next;
     const int e2 = e + step * kQueryWidth;
     if (e2 < limit) next = *reinterpret_cast<const uint4*>(src + e2);
     float x[8], o[8], y[8];
     elements_of<kPairs>(x, o, x4, me, a.rot);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], A[i], o[i] * B[i]);
     if (a.q_weight) {
-      const float n = fast_norm<D>(x, a.eps, y, o, A, B);
+      normed<D>(y, x, o, A, B, a.eps, wide);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= n;
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], A[i], o[i] * B[i]);
     }
     if (e < limit) *reinterpret_cast<uint4*>(dst + e) = pack8(y);
   }

@@ -308,9 +308,10 @@ enum { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 };
  *     where that sum is 0).
  * Equal c go to the lower expert, equal values to the lower group. c and values are FP64 and are
  * compared to 42 bits, to which c is cut and a value, the sum of c as they are, rounded (without a
- * bias c is compared by the logits, exactly); weights are formed in FP64 and rounded once. An expert whose logit or bias is -inf or NaN is never chosen and has no part
- * in any sum; +inf counts as the logits' type's largest number. Where fewer than topk experts are
- * left, the rest of the places get id -1 and weight 0; mx_moe_sort gives those no row.
+ * bias c is compared by the logits, exactly); weights are formed in FP64 and rounded once. An expert
+ * whose logit or bias is -inf or NaN is never chosen and has no part in any sum; a logit of +inf counts
+ * as its type's largest number, a bias of +inf as float32's. Where fewer than topk experts are left, the
+ * rest of the places get id -1 and weight 0; mx_moe_sort gives those no row.
  *  logits: row t's E values of logits_type at element t * logits_stride (any address of that type).
  *  bias: [E] float32, or NULL. num_rows: [1] int32 or NULL: rows from *num_rows on are padding, all
  *  of their places get id -1 and weight 0. topk_ids: [T, topk] int32, topk_weights: [T, topk] float32.

@@ -120,10 +120,9 @@ struct Key32 {
 };
 struct Key64 {
   typedef double T;
-  static constexpr T kNone = -__builtin_inf(), kLeast = -1e301;
+  static constexpr T kNone = -__builtin_inf(), kLeast = -0x1p200;  // c is finite: at most a sum of two FP32 numbers and two scores
   static __device__ __forceinline__ T of(double c, int e) {
-    c = fmin(fmax(c + 0.0, -1e300), 1e300);  // -0 becomes 0; an infinite key would be a NaN with the number in it
-    const uint64_t b = __builtin_bit_cast(uint64_t, c);
+    const uint64_t b = __builtin_bit_cast(uint64_t, c + 0.0);  // -0 becomes 0
     return __builtin_bit_cast(double, (b & ~1023ull) | (uint64_t)(b >> 63 ? e : 1023 - e));
   }
   static __device__ __forceinline__ int expert(T k) {
@@ -222,6 +221,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
     for (int v = 0; v < V; ++v) {
       bias[v] = has(v) ? a.bias[number(v)] : 0.f;
       if (!(bias[v] > -__builtin_inff())) x[v] = -__builtin_inff();
+      bias[v] = fminf(bias[v], 0x1.FFFFFEp127f);
     }
   }
   const auto masked = [&](int v) { return !(x[v] > -__builtin_inff()); };

@@ -44,7 +44,8 @@ def route(logits, topk, bias=None, sigmoid=False, groups=1, topk_groups=1, group
         ok = l > -math.inf
         if bias is not None:
             with np.errstate(invalid="ignore"):
-                ok &= np.asarray(bias, dtype=np.float64) > -math.inf
+                b = np.minimum(np.asarray(bias, dtype=np.float64), FLT_MAX)
+                ok &= b > -math.inf
         if not ok.any():
             continue
         with np.errstate(all="ignore"):
@@ -53,7 +54,7 @@ def route(logits, topk, bias=None, sigmoid=False, groups=1, topk_groups=1, group
             else:
                 s = np.where(ok, np.exp(l - l[ok].max()), 0.0)
                 s = s / s.sum()
-            full = l if bias is None else s + np.asarray(bias, dtype=np.float64)
+            full = l if bias is None else s + b
             c = truncated(full)
             by = s if bias is None and group_top == 2 else full
         left = [e for e in range(E) if ok[e]]

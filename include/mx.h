@@ -530,9 +530,9 @@ mx_status mx_kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16,
  * and, at the first row that refuses, the next token is drawn from max(p - q, 0) (p without x where
  * draft_probs is NULL; p itself where that is 0 everywhere); after the last draft it is drawn from p.
  * Drawn from w: the least j with w[0] + .. + w[j] > u * (sum of w), u = sample_random[b] in [0, 1). All
- * of this is FP64. Probabilities below 0 and NaN count as 0, and rows need not sum to 1; u below 0 or
- * NaN counts as 0 and above 1 as 1 (the last token with a weight); an accept_random that is NaN and a
- * draft outside [0, V) refuse.
+ * of this is FP64. Probabilities below 0 and NaN count as 0, +inf may not be given, and rows need not
+ * sum to 1; u below 0 or NaN counts as 0 and above 1 as 1 (the last token with a weight); an
+ * accept_random that is NaN and a draft outside [0, V) refuse.
  *  target_probs, draft_probs: row r's V float32 at element r * target_stride (r * draft_stride).
  *  tokens: [T] int32. cu_q: [B + 1] int32, non-decreasing from 0 (clamped to [0, T]). kv_lens: [B]
  *    int32, with this step's rows. accept_random: [T], sample_random: [B] float32.

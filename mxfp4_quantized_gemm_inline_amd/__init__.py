@@ -767,7 +767,10 @@ def mx_verify_drafts(target_probs, draft_probs, tokens, cu_q, kv_lens, accept_ra
     [T]) are its last token and its drafts, target_probs and draft_probs (float32 [T, V]; draft_probs None
     for drafts without chance) the distributions after each row, accept_random [T] and sample_random [B]
     (float32) the numbers in [0, 1) that decide. Returns (out_tokens int32 [T]: accepted drafts, then the
-    next token, then -1; accepted int32 [B]; new_lens int32 [B]: kv_lens less the refused drafts)."""
+    next token, then -1; accepted int32 [B]; new_lens int32 [B]: kv_lens less the refused drafts).
+
+    Where neither outputs nor workspace are given they are parts of one allocation: an output that is kept
+    keeps all of it, the workspace (mx_verify_drafts_workspace_bytes) too."""
     torch = _torch()
     i32, f32 = torch.int32, torch.float32
     T, V, p_stride = _rows2(target_probs, "target_probs", (f32,))
@@ -868,7 +871,10 @@ def mx_moe_sort(topk_ids, E: int, first_expert: int = 0, expert_offsets=None, ro
                 stream=None):
     """The tables of the grouped GEMMs and the combine for the E experts from first_expert on, from
     topk_ids (int32 [T, topk], contiguous; ids of other experts have no row): (expert_offsets int32
-    [E + 1], row_token int32 [T * topk], token_rows int32 [T, topk])."""
+    [E + 1], row_token int32 [T * topk], token_rows int32 [T, topk]).
+
+    Where neither outputs nor workspace are given they are parts of one allocation: an output that is kept
+    keeps all of it, the workspace (mx_moe_sort_workspace_bytes) too."""
     torch = _torch()
     i32 = torch.int32
     _meta(topk_ids, "topk_ids", i32)

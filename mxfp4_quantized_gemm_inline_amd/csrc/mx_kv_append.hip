@@ -12,10 +12,11 @@ namespace {
 // elements of a row, at the same place in every head that it goes through, so that its weights and angles
 // are one set of registers: with A = weight * cos and B = +-(weight of the other element) * sin an element
 // is r * (x A + other B), r = 1 / sqrt(mean + eps).
-// Bound: HBM. 16411 rows of 32 + 8 heads of 128: 86 us, 4.1 TB/s (floor 72 at a copy's 4.9); the queries
-// alone 58.5 us (4.6 TB/s), keys and values alone 28.5 (FP64 issue; floor 17.4). 101 rows 5.0 us: a
-// launch, positions, angles, heads. Queries in tiles of 16 rows x 256 bytes as keys are: 75 us. All three
-// in one workgroup kind, 16 rows of all heads: 101 us, the registers of keys for all.
+// Bound: HBM. 16411 rows of 32 + 8 heads of 128: 85 to 90 us, 4.0 TB/s (floor 72 at a copy's 4.9), of 16 + 4 heads
+// of 256, as many bytes, 93; the queries alone 51 us, keys and values alone 25 (FP64 issue; floor 17.4).
+// 101 rows 5.2 us: a launch, positions, angles, heads. 16411 rows of 1, 3, 5 query heads of 128: 11.7,
+// 13.0, 16.0 us, a wave a row whatever it holds. Queries in tiles of 16 rows x 256 bytes as keys are: 75 us
+// where they took 58. All three in one workgroup kind, 16 rows of all heads: 101 us, the registers of keys for all.
 template <int D>
 struct AppendTile {  // of keys and values
   static constexpr int kWidth = D < 128 ? 128 : D;  // elements of a row at a time
@@ -80,7 +81,8 @@ __device__ __forceinline__ double exact_norm(const float (&x)[8], float eps) {
 // the root's step). Below: with mean + eps of kLeastMean n is 2^14 at most, and what products below the normal
 // numbers lose, 2^-150 each, is less than bf16 holds. Above: sums of squares under 1e38 and coefficients
 // of up to kWide (wide: some are larger) give terms under 2^124. All else is FP64's: heads whose root mean square is
-// below 6e-5 where eps is below 4e-9, or above 1e18, and weights or scales of more than 1e18.
+// below 6e-5 where eps is below 4e-9 (with such an eps also loads that a row's heads do not fill: the lanes past them
+// hold zeros), or above 1e18, and weights or scales of more than 1e18.
 constexpr float kLeastMean = 0x1p-28f, kWide = 0x1p60f;
 template <int D>
 __device__ __forceinline__ void normed(float (&y)[8], const float (&x)[8], const float (&o)[8], const float (&A)[8], const float (&B)[8],

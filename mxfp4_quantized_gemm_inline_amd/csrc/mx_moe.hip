@@ -20,16 +20,15 @@ namespace {
 // it is put one to a lane, and each is ranked by comparing it with all of them. Where more than 64 reach
 // the bound (rows of equal logits, the largest all in a few lanes) the largest is taken topk times
 // instead.
-// Bound: instruction issue (the floor of 16411 tokens x 896 bf16 logits is 6.4 us of HBM): 17.7 us, 1.7 TB/s,
-// where the largest taken topk times took 144; 64-bit keys take 24.6 there; the bound bisected
-// down to exactly topk lanes 0.7 us more. 64 experts 8.9 us. 256 experts in 8 groups with a bias 4099 tokens
-// 10.3 us. 16 tokens 4.3 us: a launch and the chain of one token.
+// Bound: instruction issue (the floor of 16411 tokens x 896 bf16 logits is 6.4 us of HBM): 17.4 us, 1.8 TB/s,
+// where the largest taken topk times took 144; 64-bit keys take 24.6 there, and 20.9 for FP32 logits, 48 with
+// a bias; the bound bisected down to exactly topk lanes 0.7 us more. 64 experts 9.0 us. 256 experts in 8 groups
+// with a bias 4099 tokens 9.9 us. 16 tokens 4.5 us: a launch and the chain of one token.
 
 constexpr int kRouteWaves = 4;
 constexpr int kList = 64;        // keys that are ranked, at most
-// At most: the lanes that reach the bound may be a quarter more than topk, or as many as have kList keys
-// together. A quarter alone: 64, 128, 256 experts, topk 6 to 8, 16411 tokens 12.8, 13.3, 13.7 us against 8.9,
-// 11.5, 12.7; no bound for one key a lane, longer lists, 10.0 against 8.9.
+// At most. 11 / 14 / 18: 4099 tokens of 256 experts in 8 groups 11.7 / 9.9 / 10.0 us, FP32 logits of 896 experts,
+// 16411 tokens, 24.1 / 20.6 / 20.6 (fewer leave lists too long to rank), bf16 ones 17.0 at each.
 constexpr int kBisections = 14;
 
 template <int kControl, int kRows = 0xF>
@@ -301,6 +300,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
   const uint32_t c = Key::coarse(mine);
   uint32_t lo = 0, hi = wave_max(c);
   lo = ~wave_max(~c);
+  // The lanes that reach the bound may be a quarter more than topk, or as many as have kList keys together. A
+  // quarter alone: 64, 128, 256 experts, topk 6 to 8, 16411 tokens 12.8, 13.3, 13.7 us against 8.9, 11.5,
+  // 12.7; no bound for one key a lane, longer lists, 10.0 against 8.9.
   const int most = max(a.topk + a.topk / 4, kList / V);
   for (int i = 0; i < kBisections && lo < hi; ++i) {
     const uint32_t mid = lo + (hi - lo + 1) / 2;
@@ -389,9 +391,9 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
   RouteShape g = {64, a.E / a.groups};
   while (g.lanes > 64 / a.groups) g.lanes /= 2;
   const int each = (g.size + g.lanes - 1) / g.lanes, fours = (g.size + 4 * g.lanes - 1) / (4 * g.lanes);
-  // Four experts in one load where they lie so: 16411 x 896 18.2 us against 25.1 one by one, 256 tokens 5.2
-  // against 6.1; 1000 experts in 5 groups 35 against 47, with a bias 125 against 148. Of 64 and 128 experts
-  // (one or two a lane) one by one 8.9 against 10.1, 11.6 against 12.4.
+  // Four experts in one load where they lie so: 16411 x 896 17.3 us against 24.5 one by one, 256 tokens 5.0
+  // against 6.0; 16384 of 1000 experts in 5 groups 29 against 42, with a bias 105 against 116. Of 64 and 128
+  // experts (one or two a lane) one by one 8.6 against 9.9, 11.0 against 11.9.
   const auto on = [](uint64_t x) { return x % (4 * sizeof(L)) == 0; };
   const bool w4 = g.size % 4 == 0 && on((uint64_t)a.logits) && on((uint64_t)a.stride * sizeof(L)) && each > 2;
   if (w4) {

@@ -10,10 +10,11 @@ namespace {
 // handful of numbers), and sums the row that the next token is drawn from, a chunk a wave; the second
 // finds the chunk and then the token at which the running sum passes its number. Sums are FP64, in a
 // fixed order.
-// Bound: HBM where requests are many (64 rows of 131072 of p and q: 11.8 us, 5.7 TB/s, some of it from the
-// last-level cache, + 4.5; floor 13.7), else latency: one request 3.8 + 4.0 us, chains of four and five
-// loads. kStep 1024 / 2048 / 512: 64 x 131072 16.7 / 18.9 / 17.6 us, one request 7.6 / 9.3 / 8.2, 500 x
-// 5000 12.3 / 15.1 / 11.2.
+// Bound: HBM where requests are many (64 rows of 131072 of p, and of q for the 25 to 29 of them where a draft
+// is refused, 48 MB: 11.4 us, 4.2 TB/s, + 4.6; floor 9.7), else latency: one request 3.9 + 3.8 us, chains of
+// four and five loads. 150 rows of 50021 of p alone, 30 MB: 8.8 + 4.6 us, of which the way to the row (cu_q,
+// tokens, p) is 1.0; rows that begin at whole lines take as long. kStep 1024 / 2048 / 512: 64 x 131072
+// 16.7 / 18.9 / 17.6 us, one request 7.6 / 9.3 / 8.2, 500 x 5000 12.3 / 15.1 / 11.2.
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kChunks = kThreads;  // of a row, at most: one a thread of the second launch

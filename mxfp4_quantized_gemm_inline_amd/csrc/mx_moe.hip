@@ -20,15 +20,15 @@ namespace {
 // it is put one to a lane, and each is ranked by comparing it with all of them. Where more than 64 reach
 // the bound (rows of equal logits, the largest all in a few lanes) the largest is taken topk times
 // instead.
-// Bound: instruction issue (the floor of 16411 tokens x 896 bf16 logits is 6.4 us of HBM): 17.4 us, 1.8 TB/s,
-// where the largest taken topk times took 144; 64-bit keys take 24.6 there, and 20.9 for FP32 logits, 48 with
-// a bias; the bound bisected down to exactly topk lanes 0.7 us more. 64 experts 9.0 us. 256 experts in 8 groups
-// with a bias 4099 tokens 9.9 us. 16 tokens 4.5 us: a launch and the chain of one token.
+// Bound: instruction issue (the floor of 16411 tokens x 896 bf16 logits is 6.4 us of HBM): 17.2 us, 1.8 TB/s,
+// where the largest taken topk times took 144; 64-bit keys take 24.6 there, and 20.6 for FP32 logits, 46 with
+// a bias; the bound bisected down to exactly topk lanes 0.7 us more. 64 experts 8.9 us. 256 experts in 8 groups
+// with a bias 4099 tokens 9.9 us. 16 tokens 4.4 us: a launch and the chain of one token.
 
 constexpr int kRouteWaves = 4;
 constexpr int kList = 64;        // keys that are ranked, at most
-// At most. 11 / 14 / 18: 4099 tokens of 256 experts in 8 groups 11.7 / 9.9 / 10.0 us, FP32 logits of 896 experts,
-// 16411 tokens, 24.1 / 20.6 / 20.6 (fewer leave lists too long to rank), bf16 ones 17.0 at each.
+// At most. 11 / 14 / 18: 4099 tokens of 256 experts in 8 groups 11.8 / 9.9 / 9.8 us, FP32 logits of 896 experts,
+// 16411 tokens, 24.1 / 20.6 / 20.6 (fewer leave lists too long to rank), bf16 ones 17.2 at each.
 constexpr int kBisections = 14;
 
 template <int kControl, int kRows = 0xF>
@@ -250,29 +250,28 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteArgs a, Rou
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] /= sum;
   }
-  if (kGroups && k64 && a.bias) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) p[v] += (double)bias[v];
-  }
   T key[V];
+  double one = Key64::kNone, two = Key64::kNone;  // of a lane's experts the two largest that count for its group
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if constexpr (k64) key[v] = Key::of(!a.bias ? (double)fminf(x[v], kLargest) : kGroups ? p[v] : p[v] + (double)bias[v], number(v));
-    else key[v] = Key::of(fminf(x[v], kLargest), number(v));
+    if constexpr (k64) {
+      const double c = a.bias ? p[v] + (double)bias[v] : (double)fminf(x[v], kLargest);
+      key[v] = Key::of(c, number(v));
+      if (kGroups) {
+        // scores or c as they are: of two c that cancel nothing may be left of their keys' 42 bits
+        const double y = masked(v) ? Key64::kNone : a.bias || a.group_top == 1 ? c : p[v];
+        two = fmax(two, fmin(one, y));
+        one = fmax(one, y);
+      }
+    } else {
+      key[v] = Key::of(fminf(x[v], kLargest), number(v));
+    }
     if (masked(v)) key[v] = Key::kNone;
   }
   if (kGroups) {
     // each lane its group's key: the value, and of equal ones the lower group
     T best = Key::kNone;
     if constexpr (k64) {
-      double one = Key64::kNone, two = Key64::kNone;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        // scores or c as they are: of two c that cancel nothing may be left of their keys' 42 bits
-        const double y = masked(v) ? Key64::kNone : scored ? p[v] : Key64::value(key[v]);
-        two = fmax(two, fmin(one, y));
-        one = fmax(one, y);
-      }
       for (int d = 1; d < lanes; d <<= 1) {
         const double y = __shfl_xor(one, d), z = __shfl_xor(two, d);
         two = fmax(fmax(two, z), fmin(one, y));
@@ -391,9 +390,9 @@ hipError_t route(const RouteArgs& a, hipStream_t st) {
   RouteShape g = {64, a.E / a.groups};
   while (g.lanes > 64 / a.groups) g.lanes /= 2;
   const int each = (g.size + g.lanes - 1) / g.lanes, fours = (g.size + 4 * g.lanes - 1) / (4 * g.lanes);
-  // Four experts in one load where they lie so: 16411 x 896 17.3 us against 24.5 one by one, 256 tokens 5.0
-  // against 6.0; 16384 of 1000 experts in 5 groups 29 against 42, with a bias 105 against 116. Of 64 and 128
-  // experts (one or two a lane) one by one 8.6 against 9.9, 11.0 against 11.9.
+  // Four experts in one load where they lie so: 16411 x 896 17.2 us against 24.3 one by one, 256 tokens 5.0
+  // against 5.9; 16384 of 1000 experts in 5 groups 29 against 42, with a bias 121 against 144. Of 64 and 128
+  // experts (one or two a lane) one by one 8.5 against 9.7, 11.0 against 11.9.
   const auto on = [](uint64_t x) { return x % (4 * sizeof(L)) == 0; };
   const bool w4 = g.size % 4 == 0 && on((uint64_t)a.logits) && on((uint64_t)a.stride * sizeof(L)) && each > 2;
   if (w4) {
